@@ -24,12 +24,18 @@ __all__ = [
     "tt_selftest_timeout",
     "profile_table", "KERNEL_KINDS",
     "TT_WS_ATTN", "TT_WS_ADALN", "TT_WS_VOCAB", "TT_WS_LOOP",
+    "Q8", "q8", "tt_block_denoise_attn_q8", "tt_append_ctx_q8", "tt_quantize_rows_i8",
+    "tt_linear_i8", "tt_linear_i8_workspace_bytes", "linear_i8_workspace",
+    "tt_vocab_confidence_commit_i8",
+    "TT_WS_ATTN_Q8", "TT_WS_APPEND_Q8", "TT_WS_VOCAB_I8", "TT_Q8_INT8", "TT_Q8_E4M3",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 lib_path = os.path.join(_HERE, "libtwotower.so")
 
 TT_WS_ATTN, TT_WS_ADALN, TT_WS_VOCAB, TT_WS_LOOP = 0, 1, 2, 3
+TT_WS_ATTN_Q8, TT_WS_APPEND_Q8, TT_WS_VOCAB_I8 = 4, 5, 6
+TT_Q8_INT8, TT_Q8_E4M3 = 0, 1
 STATUS = {0: "TT_OK", 1: "TT_ERR_INVALID_ARG", 2: "TT_ERR_UNSUPPORTED", 3: "TT_ERR_WORKSPACE",
           4: "TT_ERR_CUDA", 5: "TT_ERR_TIMEOUT", 6: "TT_ERR_INTERNAL"}
 
@@ -40,10 +46,13 @@ EXPORTS = (
     "tt_adaln_modulate",
     "tt_vocab_confidence_commit", "tt_denoise_block_loop", "tt_profile_enable", "tt_profile_read",
     "tt_vocab_confidence_commit_noalloc", "tt_selftest_timeout", "tt_denoise_block_loop_layers",
-    "tt_decode_blocks", "tt_loop_last_step",
+    "tt_decode_blocks", "tt_loop_last_step", "tt_block_denoise_attn_q8", "tt_append_ctx_q8",
+    "tt_quantize_rows_i8", "tt_linear_i8_workspace_bytes", "tt_linear_i8",
+    "tt_vocab_confidence_commit_i8",
 )
 KERNEL_KINDS = ("plan", "embed", "gemm_qkv", "attn", "merge", "adaln", "gemm_vocab", "commit",
-                "gather", "init", "splitk_reduce", "append", "attn_plan")
+                "gather", "init", "splitk_reduce", "append", "attn_plan", "attn_q8", "merge_q8",
+                "append_q8", "quant_i8", "gemm_i8", "gemm_vocab_i8")
 
 
 class TTError(RuntimeError):
@@ -54,6 +63,15 @@ class TTError(RuntimeError):
 
 class Dims(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("B", "S", "Hq", "Hkv", "dh", "H", "V", "L_cap")]
+
+
+class Q8(ctypes.Structure):
+    """Format of an 8-bit context cache (tt_q8): element type and positions per scale."""
+    _fields_ = [("type", ctypes.c_int32), ("block", ctypes.c_int32)]
+
+
+class _RowStrides(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("batch", "token", "head")]
 
 
 _P = ctypes.c_void_p
@@ -114,6 +132,23 @@ def lib() -> ctypes.CDLL:
         L.tt_denoise_block_loop_layers.argtypes = (
             [ctypes.POINTER(Dims), ctypes.c_int32] + [_P] * 8
             + [ctypes.c_float, ctypes.c_float, ctypes.c_int32] + [_P] * 5
+            + [_P, ctypes.c_size_t, _P])
+        dims_p, q8_p = ctypes.POINTER(Dims), ctypes.POINTER(Q8)
+        L.tt_block_denoise_attn_q8.restype = ctypes.c_int
+        L.tt_block_denoise_attn_q8.argtypes = [dims_p, q8_p] + [_P] * 9 + [_P, ctypes.c_size_t, _P]
+        L.tt_append_ctx_q8.restype = ctypes.c_int
+        L.tt_append_ctx_q8.argtypes = (
+            [dims_p, q8_p, ctypes.c_int32, _P, _P, _P, ctypes.POINTER(_RowStrides)] + [_P] * 5
+            + [_P, ctypes.c_size_t, _P])
+        L.tt_quantize_rows_i8.restype = ctypes.c_int
+        L.tt_quantize_rows_i8.argtypes = [ctypes.c_int32, ctypes.c_int32] + [_P] * 4
+        L.tt_linear_i8_workspace_bytes.restype = ctypes.c_size_t
+        L.tt_linear_i8_workspace_bytes.argtypes = [ctypes.c_int32] * 3
+        L.tt_linear_i8.restype = ctypes.c_int
+        L.tt_linear_i8.argtypes = [ctypes.c_int32] * 3 + [_P] * 5 + [ctypes.c_size_t, _P]
+        L.tt_vocab_confidence_commit_i8.restype = ctypes.c_int
+        L.tt_vocab_confidence_commit_i8.argtypes = (
+            [dims_p, _P, _P, _P, ctypes.c_float, ctypes.c_float] + [_P] * 5
             + [_P, ctypes.c_size_t, _P])
         _lib = L
     return _lib
@@ -376,3 +411,126 @@ def tt_loop_last_step(d: Dims, ws, y_rows, row_ids, conf, argmax, stream=None) -
         _sized(argmax, "argmax", rows * 4), ctypes.addressof(n), _stream(stream)),
         "tt_loop_last_step")
     return int(n.value)
+
+
+# --------------------------------------------------------------- 8-bit serving
+def q8(kind: str, block: int) -> Q8:
+    """Format of an 8-bit context cache: kind "int8" or "e4m3", `block` context
+    positions (16, 32, 64 or 128) per scale."""
+    return Q8({"int8": TT_Q8_INT8, "e4m3": TT_Q8_E4M3}[kind], int(block))
+
+
+def _one_device(*tensors) -> None:
+    """Refuses tensors that are not on the current device: the kernels are
+    launched there, on its current stream unless another is given."""
+    import torch
+    cur = None
+    for t in tensors:
+        if t is None or isinstance(t, int) or not t.is_cuda:
+            continue
+        if cur is None:
+            cur = torch.cuda.current_device()
+        if t.get_device() != cur:
+            raise ValueError(f"tensor on cuda:{t.get_device()}, current device is cuda:{cur}")
+
+
+def _n_scales(d: Dims, f: Q8) -> int:
+    return d.B * d.Hkv * -(-d.L_cap // max(f.block, 1))
+
+
+def tt_block_denoise_attn_q8(d: Dims, f: Q8, q_blk, k_blk, v_blk, k_ctx, v_ctx, k_scale, v_scale,
+                             ctx_len, out, ws, stream=None) -> None:
+    """tt_block_denoise_attn over a context cache held in 8 bits: codes
+    [B, Hkv, L_cap, dh] (int8 or float8_e4m3fn) and one float32 scale per
+    `f.block` positions and KV head."""
+    rows, ctx, ns = d.B * d.S, d.B * d.Hkv * d.L_cap * d.dh, _n_scales(d, f) * 4
+    _one_device(q_blk, k_blk, v_blk, k_ctx, v_ctx, k_scale, v_scale, ctx_len, out, ws)
+    _check(lib().tt_block_denoise_attn_q8(
+        ctypes.byref(d), ctypes.byref(f), _sized(q_blk, "q_blk", rows * d.Hq * d.dh * 2),
+        _sized(k_blk, "k_blk", rows * d.Hkv * d.dh * 2),
+        _sized(v_blk, "v_blk", rows * d.Hkv * d.dh * 2), _sized(k_ctx, "k_ctx", ctx),
+        _sized(v_ctx, "v_ctx", ctx), _sized(k_scale, "k_scale", ns),
+        _sized(v_scale, "v_scale", ns), _sized(ctx_len, "ctx_len", d.B * 4),
+        _sized(out, "out", rows * d.Hq * d.dh * 2), _ptr(ws), _nbytes(ws), _stream(stream)),
+        "tt_block_denoise_attn_q8")
+
+
+def _rows_arg(x, name: str, d: Dims, n: int) -> int:
+    """Address of a strided [B, n, Hkv, dh] bf16 tensor with a dense last dimension."""
+    if not x.is_cuda:
+        raise ValueError("libtwotower takes CUDA tensors only (no CPU path)")
+    if tuple(x.shape) != (d.B, n, d.Hkv, d.dh) or x.element_size() != 2 or \
+            (x.stride(3) != 1 and d.dh > 1):
+        raise ValueError(f"{name} must be a 16-bit tensor of shape {(d.B, n, d.Hkv, d.dh)} with a "
+                         f"dense last dimension; got {tuple(x.shape)}, strides {x.stride()}")
+    return x.data_ptr()
+
+
+def tt_append_ctx_q8(d: Dims, f: Q8, n: int, new_len, k_new, v_new, k_ctx, v_ctx, k_scale, v_scale,
+                     ctx_len, ws, stream=None) -> None:
+    """Quantise the first new_len[b] (or all n, with new_len None) rows of
+    k_new / v_new [B, n, Hkv, dh] onto the end of each sequence's 8-bit cache;
+    ctx_len grows in place.  k_new and v_new may be strided views (the last
+    dimension dense, both with the same strides)."""
+    ctx, ns = d.B * d.Hkv * d.L_cap * d.dh, _n_scales(d, f) * 4
+    k_ptr, v_ptr = _rows_arg(k_new, "k_new", d, n), _rows_arg(v_new, "v_new", d, n)
+    sk, sv = k_new.stride(), v_new.stride()
+    # a dimension of one element has no stride of its own
+    st = [0 if size == 1 else a for size, a in zip(k_new.shape, sk)][:3]
+    if st != [0 if size == 1 else a for size, a in zip(v_new.shape, sv)][:3]:
+        raise ValueError(f"k_new and v_new need the same strides; got {sk} and {sv}")
+    _one_device(new_len, k_new, v_new, k_ctx, v_ctx, k_scale, v_scale, ctx_len, ws)
+    _check(lib().tt_append_ctx_q8(
+        ctypes.byref(d), ctypes.byref(f), int(n), _sized(new_len, "new_len", d.B * 4), k_ptr, v_ptr,
+        ctypes.byref(_RowStrides(*st)), _sized(k_ctx, "k_ctx", ctx), _sized(v_ctx, "v_ctx", ctx),
+        _sized(k_scale, "k_scale", ns), _sized(v_scale, "v_scale", ns),
+        _sized(ctx_len, "ctx_len", d.B * 4), _ptr(ws), _nbytes(ws), _stream(stream)),
+        "tt_append_ctx_q8")
+
+
+def tt_quantize_rows_i8(rows: int, K: int, x, q, scale, stream=None) -> None:
+    """int8 codes q [rows, K] and float32 scales [rows] of bf16 x [rows, K]
+    (weights: a row per output channel)."""
+    _one_device(x, q, scale)
+    _check(lib().tt_quantize_rows_i8(
+        int(rows), int(K), _sized(x, "x", rows * K * 2), _sized(q, "q", rows * K),
+        _sized(scale, "scale", rows * 4), _stream(stream)), "tt_quantize_rows_i8")
+
+
+def tt_linear_i8_workspace_bytes(rows: int, N: int, K: int) -> int:
+    n = lib().tt_linear_i8_workspace_bytes(int(rows), int(N), int(K))
+    if n == 0:
+        raise TTError(1, "tt_linear_i8_workspace_bytes", tt_last_error())
+    return int(n)
+
+
+def linear_i8_workspace(rows: int, N: int, K: int, device="cuda"):
+    """A torch uint8 device buffer of tt_linear_i8_workspace_bytes(rows, N, K) bytes."""
+    import torch
+    return torch.empty(tt_linear_i8_workspace_bytes(rows, N, K), dtype=torch.uint8, device=device)
+
+
+def tt_linear_i8(rows: int, N: int, K: int, x, w_q, w_scale, out, ws, stream=None) -> None:
+    """out [rows, N] = bf16(x [rows, K] . (w_q * w_scale)^T), x quantised per
+    row to int8, the sums exact in 32-bit integers."""
+    _one_device(x, w_q, w_scale, out, ws)
+    _check(lib().tt_linear_i8(
+        int(rows), int(N), int(K), _sized(x, "x", rows * K * 2), _sized(w_q, "w_q", N * K),
+        _sized(w_scale, "w_scale", N * 4), _sized(out, "out", rows * N * 2), _ptr(ws), _nbytes(ws),
+        _stream(stream)), "tt_linear_i8")
+
+
+def tt_vocab_confidence_commit_i8(d: Dims, y, w_q, w_scale, gamma: float, logit_scale: float,
+                                  tokens, masked, conf_out, argmax_out, n_committed, ws,
+                                  stream=None) -> None:
+    """tt_vocab_confidence_commit with int8 weights w_q [V, H], one float32
+    scale per token, and y quantised per row."""
+    rows = d.B * d.S
+    _one_device(y, w_q, w_scale, tokens, masked, conf_out, argmax_out, n_committed, ws)
+    _check(lib().tt_vocab_confidence_commit_i8(
+        ctypes.byref(d), _sized(y, "y", rows * d.H * 2), _sized(w_q, "w_q", d.V * d.H),
+        _sized(w_scale, "w_scale", d.V * 4), float(gamma), float(logit_scale),
+        _sized(tokens, "tokens", rows * 4), _sized(masked, "masked", rows),
+        _sized(conf_out, "conf_out", rows * 4), _sized(argmax_out, "argmax_out", rows * 4),
+        _sized(n_committed, "n_committed", d.B * 4), _ptr(ws), _nbytes(ws), _stream(stream)),
+        "tt_vocab_confidence_commit_i8")

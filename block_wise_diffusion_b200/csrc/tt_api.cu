@@ -13,6 +13,7 @@
 #include <vector>
 
 #include "tt_internal.h"
+#include "tt_q8.h"
 
 namespace tt {
 
@@ -163,17 +164,24 @@ static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-bool make_tmap_2d(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer,
-                  uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer) {
+bool make_tmap_2d_type(CUtensorMap* m, CUtensorMapDataType type, const void* base, uint64_t inner,
+                       uint64_t outer, uint64_t row_bytes, uint32_t box_inner,
+                       uint32_t box_outer) {
   auto fn = encode_fn();
   if (fn == nullptr) return false;
   cuuint64_t dims[2] = {inner, outer};
   cuuint64_t strides[1] = {row_bytes};
   cuuint32_t box[2] = {box_inner, box_outer};
   cuuint32_t es[2] = {1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,
-            es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  return fn(m, type, 2, const_cast<void*>(base), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool make_tmap_2d(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer,
+                  uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer) {
+  return make_tmap_2d_type(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, inner, outer, row_bytes,
+                           box_inner, box_outer);
 }
 
 bool make_tmap_3d(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
@@ -377,6 +385,13 @@ static tt_status check_ws(const tt_dims& d, int which, void* ws, size_t ws_bytes
 }
 
 tt_status set_error(tt_status s, const char* msg) { return fail(s, "%s", msg); }
+tt_status set_errorf(tt_status s, const char* fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(g_err, sizeof g_err, fmt, ap);
+  va_end(ap);
+  return s;
+}
 tt_status check_dims_public(const tt_dims* d) { return check_dims(d); }
 
 // ---------------------------------------------------------- stage helpers
@@ -741,6 +756,7 @@ tt_status tt_set_attn_splits(int32_t n_splits) {
 
 size_t tt_workspace_bytes(const tt_dims* d, int which) {
   if (check_dims(d) != TT_OK) return 0;
+  if (which >= TT_WS_ATTN_Q8 && which <= TT_WS_VOCAB_I8) return q8_workspace_bytes(*d, which);
   if (which < TT_WS_ATTN || which > TT_WS_LOOP) {
     fail(TT_ERR_INVALID_ARG, "unknown workspace kind %d", which);
     return 0;

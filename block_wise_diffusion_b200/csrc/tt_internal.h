@@ -198,6 +198,7 @@ struct CommitArgs {
   float2* rowres;       // [B*S] (confidence, token bits) of each row
   int* seqcnt;          // [B] finished CTAs per sequence; zero before the call, left zero
   const float4* stats;  // [compact row][n_vt] tile statistics of the vocab GEMM
+  const float* row_scale;  // optional [compact row]: factor of scale_log2 for that row
   float scale_log2;
   float gamma;
   const int* rowlist;   // compact row -> b*S+s, then b*S+s -> compact row (at B*S + row)
@@ -233,14 +234,18 @@ cudaError_t launch_loop_init(int B, int S, int* steps_taken, int* commit_step, i
 // library loads without a GPU driver present).
 bool make_tmap_2d(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer,
                   uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer);
+bool make_tmap_2d_type(CUtensorMap* m, CUtensorMapDataType type, const void* base, uint64_t inner,
+                       uint64_t outer, uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer);
 bool make_tmap_3d(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
                   uint64_t stride1_bytes, uint64_t stride2_bytes, uint32_t b0, uint32_t b1,
                   uint32_t b2);
 
 void count_launch(int n = 1);
 
-// Record `msg` as the calling thread's last error and return `s`.
+// Record `msg` (or a printf-style text) as the calling thread's last error and
+// return `s`.
 tt_status set_error(tt_status s, const char* msg);
+tt_status set_errorf(tt_status s, const char* fmt, ...);
 // The shape checks of the public entry points.
 tt_status check_dims_public(const tt_dims* d);
 

@@ -1,0 +1,67 @@
+// Internal definitions of the 8-bit serving operators.
+#pragma once
+#include "tt_internal.h"
+
+namespace tt {
+
+// ------------------------------------------------------------ cache append
+struct AppendQ8Args {
+  int B, Hkv, dh, L_cap, n, block, n_blocks;  // n_blocks: scales per (sequence, head)
+  const int* new_len;                         // optional [B]
+  const uint16_t *k_new, *v_new;
+  long long stride_b, stride_t, stride_h;     // elements
+  uint8_t *k_ctx, *v_ctx;
+  float *k_scale, *v_scale;
+  int* ctx_len;
+  int* err;
+};
+cudaError_t launch_append_q8(const AppendQ8Args& a, int type, cudaStream_t st);
+
+// Row r < rows (or < *M_dev) of x, or row rowlist[r] of it: int8 codes q[r, :]
+// and scale[r].
+cudaError_t launch_quant_rows(const uint16_t* x, int K, int8_t* q, float* scale,
+                              const int* rowlist, const int* M_dev, int rows, cudaStream_t st);
+
+// ------------------------------------------------------- integer products
+// C = A[M, K] . B[N, K]^T, both int8 and K-major, 128 rows x 128 bytes of K
+// per tile.
+constexpr int kI8BM = 128, kI8BK = 128;
+constexpr int kI8VocabBN = kVocabBN, kI8VocabStages = 5;
+constexpr int kI8BN = 256, kI8Stages = 4;
+struct GemmI8Args {
+  int M_alloc;           // rows of A
+  const int* M_dev;      // device row count (nullptr: M_alloc)
+  int N, K;
+  const float* a_scale;  // [M]
+  const float* b_scale;  // [N]
+  float4* stats;         // vocabulary: [row][ceil(N / kI8VocabBN)], as GemmArgs::stats
+  float scale_log2;      // vocabulary: logit_scale * log2(e)
+  uint16_t* C;           // linear: bf16 [M, N]
+  int* err;
+};
+cudaError_t launch_gemm_i8_vocab(const CUtensorMap& tmA, const CUtensorMap& tmB,
+                                 const GemmI8Args& a, int grid, cudaStream_t st);
+cudaError_t launch_gemm_i8_linear(const CUtensorMap& tmA, const CUtensorMap& tmB,
+                                  const GemmI8Args& a, int grid, cudaStream_t st);
+
+// --------------------------------------------------------------- attention
+struct AttnQ8Args {
+  int B, S, Hq, Hkv, dh, G, L_cap, block, n_blocks;
+  const uint16_t *q, *k_blk, *v_blk;
+  const uint8_t *k_ctx, *v_ctx;
+  const float *k_scale, *v_scale;
+  const int* ctx_len;
+  float scale_log2;  // log2(e) / sqrt(dh)
+  uint16_t* out;
+  int* err;
+};
+cudaError_t launch_attn_q8(const AttnQ8Args& a, int type, cudaStream_t st);
+
+// Workspace bytes of the 8-bit calls of tt_workspace_bytes (d already checked).
+size_t q8_workspace_bytes(const tt_dims& d, int which);
+
+// 2-D map of bytes, 128-byte swizzle.
+bool make_tmap_2d_u8(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer,
+                     uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer);
+
+}  // namespace tt

@@ -493,9 +493,10 @@ __global__ void __launch_bounds__(kCommitThreads) commit_kernel(const CommitArgs
   const int row = blockIdx.x, b = row / S;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int M = a.M_dev != nullptr ? *a.M_dev : a.B * S;
-  const float c = a.scale_log2;
   if (a.masked[row] != 0) {
     const int j = a.rowlist[a.B * S + row];  // this row's compact index
+    const float c =
+        a.scale_log2 * (a.row_scale != nullptr && j >= 0 && j < M ? a.row_scale[j] : 1.f);
     RowBest rb{-INFINITY, 0.f, 0x7fffffff, -1};
     if (j >= 0 && j < M) {
       // thread i reads tiles i, i + kCommitThreads, ...: all loads first

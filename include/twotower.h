@@ -68,7 +68,12 @@ typedef struct {
 } tt_dims;
 
 /* Which call a workspace is sized for. */
-enum { TT_WS_ATTN = 0, TT_WS_ADALN = 1, TT_WS_VOCAB = 2, TT_WS_LOOP = 3 };
+enum {
+  TT_WS_ATTN = 0, TT_WS_ADALN = 1, TT_WS_VOCAB = 2, TT_WS_LOOP = 3,
+  TT_WS_ATTN_Q8 = 4,   /* tt_block_denoise_attn_q8 */
+  TT_WS_APPEND_Q8 = 5, /* tt_append_ctx_q8 */
+  TT_WS_VOCAB_I8 = 6   /* tt_vocab_confidence_commit_i8 */
+};
 
 /* Human-readable name of a status code (static string). */
 TT_API const char* tt_status_string(tt_status s);
@@ -116,7 +121,9 @@ TT_API tt_status tt_set_loop_graphs(int32_t on);
 enum {
   TT_K_PLAN = 0, TT_K_EMBED = 1, TT_K_GEMM_QKV = 2, TT_K_ATTN = 3, TT_K_MERGE = 4,
   TT_K_ADALN = 5, TT_K_GEMM_VOCAB = 6, TT_K_COMMIT = 7, TT_K_GATHER = 8, TT_K_INIT = 9,
-  TT_K_REDUCE = 10, TT_K_APPEND = 11, TT_K_ATTN_PLAN = 12, TT_K_COUNT = 13
+  TT_K_REDUCE = 10, TT_K_APPEND = 11, TT_K_ATTN_PLAN = 12, TT_K_ATTN_Q8 = 13,
+  TT_K_MERGE_Q8 = 14, TT_K_APPEND_Q8 = 15, TT_K_QUANT_I8 = 16, TT_K_GEMM_I8 = 17,
+  TT_K_GEMM_VOCAB_I8 = 18, TT_K_COUNT = 19
 };
 
 /* Per-kernel profiler: while enabled, every kernel this library launches is
@@ -385,6 +392,143 @@ TT_API tt_status tt_vocab_confidence_commit_noalloc(const tt_dims* d, const tt_b
                                                     uint8_t* masked, float* conf_out,
                                                     int32_t* argmax_out, int32_t* n_committed,
                                                     void* stream);
+
+/* ------------------------------------------------------------ 8-bit serving
+ * The calls below hold the context cache, the linear update's weights and the
+ * vocabulary projection's weights in 8 bits.  Scales are float32.  Two rules
+ * are common to them:
+ *  - the scale of a group of values x (a row of a product, or a block of a
+ *    cache) is s = max(max|x| * r, 2^-60), one float32 product with r the
+ *    float32 nearest 1 / qmax; qmax = 127 for int8, 448 for e4m3;
+ *  - the code of x is x / s rounded to the nearest code, ties to even, as if
+ *    the quotient were exact.  int8 codes lie in -127..127; -128 is never
+ *    written, but read as -128 where a caller stores it.
+ * A group that holds an infinity or a NaN gets the scale NaN and codes 0, so
+ * every result computed from it is NaN. */
+
+/* Element types of an 8-bit context cache. */
+enum { TT_Q8_INT8 = 0, TT_Q8_E4M3 = 1 };
+
+/* Format of an 8-bit context cache: `type` is TT_Q8_INT8 or TT_Q8_E4M3;
+ * `block` in {16, 32, 64, 128} is the number of consecutive context positions
+ * (from a multiple of `block`) of one KV head that share one scale.  K and V
+ * have scales of their own. */
+typedef struct {
+  int32_t type, block;
+} tt_q8;
+
+/*
+ * tt_block_denoise_attn over an 8-bit context cache: the same operation with
+ *   key_j = k_scale[b,g,j/block] * k_ctx[b,g,j,:] and the matching values for
+ * the context positions j < ctx_len[b]; the block's own keys and values stay
+ * bf16.  Scores, softmax statistics and the output are accumulated in fp32;
+ * the probabilities are rounded to fp16 for the product with V.  The result
+ * is the bf16 rounding of that.
+ *
+ *   f               format of the cache
+ *   q_blk, k_blk, v_blk, ctx_len, out   as in tt_block_denoise_attn
+ *   k_ctx, v_ctx    8-bit codes [B, Hkv, L_cap, dh], 16-byte aligned (codes
+ *                   and scales may be NULL when L_cap is 0)
+ *   k_scale, v_scale  float [B, Hkv, ceil(L_cap / block)]; those of blocks
+ *                   that hold a position below ctx_len[b] are finite and > 0
+ *                   (v_scale at least 2^-60, as tt_append_ctx_q8 writes them);
+ *                   other scales and codes are never used
+ *   ws              workspace of at least tt_workspace_bytes(d, TT_WS_ATTN_Q8)
+ * A ctx_len outside 0..L_cap is clamped and recorded (TT_ERR_INVALID_ARG).
+ * Calls that may overlap on the GPU need workspaces of their own.
+ */
+TT_API tt_status tt_block_denoise_attn_q8(const tt_dims* d, const tt_q8* f, const tt_bf16* q_blk,
+                                          const tt_bf16* k_blk, const tt_bf16* v_blk,
+                                          const void* k_ctx, const void* v_ctx,
+                                          const float* k_scale, const float* v_scale,
+                                          const int32_t* ctx_len, tt_bf16* out, void* ws,
+                                          size_t ws_bytes, void* stream);
+
+/* Element strides of rows [B, n, Hkv, dh] (the last dimension is dense): the
+ * distance between sequences, between tokens and between KV heads.  Multiples
+ * of 8. */
+typedef struct {
+  int64_t batch, token, head;
+} tt_row_strides;
+
+/*
+ * Rows join an 8-bit context cache: a committed block, or a whole prompt.
+ * For every sequence b the first m_b rows (m_b = new_len[b], or n when
+ * new_len is NULL) are quantised to context positions ctx_len[b] ..
+ * ctx_len[b] + m_b - 1 of every KV head and ctx_len[b] += m_b.
+ * Scales: a block that starts at or past ctx_len[b] gets the scale of its new
+ * rows.  The block that holds older rows keeps its scale where that is at
+ * least the new rows' own; otherwise it takes theirs, and the older codes c
+ * become the nearest code of c * s_old / s_new (exact quotient, ties to
+ * even).  No other code or scale is written.
+ *
+ *   d        B, Hkv, dh and L_cap are used; the other sizes only have to be valid
+ *   n        rows per sequence in k_new and v_new, 1 .. L_cap
+ *   new_len  int32 [B] device, or NULL; values outside 0..n are recorded
+ *   k_new, v_new  bf16, element (b, i, g, e) at b*batch + i*token + g*head + e
+ *            of `strides` (so they can be column ranges of one projection's
+ *            rows, or a bf16 context cache); rows at or past m_b are not read
+ *   k_ctx, v_ctx, k_scale, v_scale   as in tt_block_denoise_attn_q8, IN/OUT
+ *   ctx_len  int32 [B] device, IN/OUT
+ *   ws       workspace of at least tt_workspace_bytes(d, TT_WS_APPEND_Q8)
+ * A sequence whose ctx_len or new_len is out of range, or that has no room
+ * (ctx_len[b] + m_b > L_cap), is left unchanged and TT_ERR_INVALID_ARG is
+ * recorded (tt_device_status); the others are appended.
+ */
+TT_API tt_status tt_append_ctx_q8(const tt_dims* d, const tt_q8* f, int32_t n,
+                                  const int32_t* new_len, const tt_bf16* k_new,
+                                  const tt_bf16* v_new, const tt_row_strides* strides,
+                                  void* k_ctx, void* v_ctx, float* k_scale, float* v_scale,
+                                  int32_t* ctx_len, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Rows in 8-bit integers with a scale for each: the weights of the two calls
+ * below (a row per output channel), by the rules above.
+ *
+ *   x      bf16 [rows, K]    q  int8 [rows, K]    scale  float [rows]
+ * rows in 1 .. 2^24 - 1; K a multiple of 16, 16 .. 131072.
+ */
+TT_API tt_status tt_quantize_rows_i8(int32_t rows, int32_t K, const tt_bf16* x, int8_t* q,
+                                     float* scale, void* stream);
+
+/* Bytes of workspace tt_linear_i8 needs (0 for sizes that it refuses). */
+TT_API size_t tt_linear_i8_workspace_bytes(int32_t rows, int32_t N, int32_t K);
+
+/*
+ * Linear update in 8-bit integers: each row of x is quantised by the rules
+ * above (scale xs, codes xq), and
+ *   out[r, c] = bf16( xs[r] * w_scale[c] * sum_k xq[r, k] * w_q[c, k] ),
+ * the sum in 32-bit integers (exact), the scales applied in fp32.
+ *
+ *   x        bf16 [rows, K];  w_q  int8 [N, K] (output-major, as u_t)
+ *   w_scale  float [N] (16-byte aligned);  out  bf16 [rows, N]
+ *   ws       workspace of at least tt_linear_i8_workspace_bytes(rows, N, K)
+ * rows and N in 1 .. 2^24 - 1; K a multiple of 16, 16 .. 131072 (the largest
+ * whose sum of 128 * 127 * K still fits 32 bits is above it).
+ */
+TT_API tt_status tt_linear_i8(int32_t rows, int32_t N, int32_t K, const tt_bf16* x,
+                              const int8_t* w_q, const float* w_scale, tt_bf16* out, void* ws,
+                              size_t ws_bytes, void* stream);
+
+/*
+ * tt_vocab_confidence_commit with the vocabulary projection in 8-bit
+ * integers: the masked rows of y are quantised by the rules above (scale ys,
+ * codes yq) and
+ *   logits = logit_scale * ys[r] * w_scale[v] * sum_k yq[r, k] * w_q[v, k],
+ * the sum exact in 32-bit integers.  The argmax compares w_scale[v] * sum in
+ * fp32 (ys[r] and logit_scale are common to a row), lowest id on ties; the
+ * commit rule, the outputs and the errors are those of
+ * tt_vocab_confidence_commit.
+ *
+ *   w_q      int8 [V, H];  w_scale  float [V] (16-byte aligned), finite
+ *   ws       workspace of at least tt_workspace_bytes(d, TT_WS_VOCAB_I8)
+ */
+TT_API tt_status tt_vocab_confidence_commit_i8(const tt_dims* d, const tt_bf16* y,
+                                               const int8_t* w_q, const float* w_scale,
+                                               float gamma, float logit_scale, int32_t* tokens,
+                                               uint8_t* masked, float* conf_out,
+                                               int32_t* argmax_out, int32_t* n_committed,
+                                               void* ws, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }
