@@ -271,6 +271,11 @@ static AttnGeom attn_geom(const tt_dims& d) {
   return g;
 }
 
+AttnShape attn_shape(const tt_dims& d) {
+  const AttnGeom g = attn_geom(d);
+  return AttnShape{g.G, g.s_per_half, g.rows_per_half, g.halves, g.n_qtiles, g.units, g.n_ctas};
+}
+
 // K splits of the linear-update GEMM: enough (tile, K range) units to fill
 // the SMs when the block has few rows; a power of two dividing H/64.
 static int ksplit_for(const tt_dims& d, int n_out) {

@@ -70,6 +70,28 @@ struct Carver {
   size_t total() const { return (off + 255) & ~size_t(255); }
 };
 
+// -------------------------------------------------------------- attention
+struct AttnQ8Ws {
+  int *ctrl, *tile_start, *first_unit, *unit_done;
+  int4* unit_ctas;
+  float *part_o, *part_ml;
+  size_t total;
+};
+AttnQ8Ws carve_attn(const tt_dims& d, const AttnShape& g, void* ws) {
+  Carver c{reinterpret_cast<uint8_t*>(ws)};
+  AttnQ8Ws w;
+  const size_t slots = (size_t)g.units + g.n_ctas - 1;
+  w.ctrl = c.take<int>(kCtrlBytes);
+  w.tile_start = c.take<int>((size_t)(g.units + 1) * sizeof(int));
+  w.first_unit = c.take<int>((size_t)g.n_ctas * sizeof(int));
+  w.unit_ctas = c.take<int4>((size_t)g.units * sizeof(int4));
+  w.unit_done = c.take<int>((size_t)g.units * sizeof(int));
+  w.part_o = c.take<float>(slots * 256 * d.dh * sizeof(float));
+  w.part_ml = c.take<float>(slots * 256 * 2 * sizeof(float));
+  w.total = c.total();
+  return w;
+}
+
 // ------------------------------------------------------------- vocabulary
 struct VocabWs {
   int *ctrl, *seqcnt, *rowlist;
@@ -143,6 +165,7 @@ bool make_tmap_2d_u8(CUtensorMap* m, const void* base, uint64_t inner, uint64_t 
 
 size_t q8_workspace_bytes(const tt_dims& d, int which) {
   if (which == TT_WS_VOCAB_I8) return carve_vocab(d, nullptr).total;
+  if (which == TT_WS_ATTN_Q8) return carve_attn(d, attn_shape(d), nullptr).total;
   return kCtrlBytes;
 }
 
@@ -170,7 +193,9 @@ tt_status tt_block_denoise_attn_q8(const tt_dims* d, const tt_q8* f, const tt_bf
   }
   Q8_CHECK(check_ptr(ctx_len, "ctx_len", 4));
   Q8_CHECK(check_ptr(out, "out", 16));
-  Q8_CHECK(check_ws_ptr(ws, ws_bytes, q8_workspace_bytes(*d, TT_WS_ATTN_Q8)));
+  const AttnShape g = attn_shape(*d);
+  const AttnQ8Ws w = carve_attn(*d, g, ws);
+  Q8_CHECK(check_ws_ptr(ws, ws_bytes, w.total));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   AttnQ8Args a{};
   a.B = d->B;
@@ -192,9 +217,34 @@ tt_status tt_block_denoise_attn_q8(const tt_dims* d, const tt_q8* f, const tt_bf
   a.ctx_len = ctx_len;
   a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)d->dh));
   a.out = out;
-  a.err = static_cast<int*>(ws);
-  Q8_CUDA(cudaMemsetAsync(ws, 0, kCtrlBytes, st));
+  a.s_per_half = g.s_per_half;
+  a.rows_per_half = g.rows_per_half;
+  a.halves = g.halves;
+  a.n_qtiles = g.n_qtiles;
+  a.units = g.units;
+  a.n_ctas = g.n_ctas;
+  a.tile_start = w.tile_start;
+  a.first_unit = w.first_unit;
+  a.unit_ctas = w.unit_ctas;
+  a.part_o = w.part_o;
+  a.part_ml = w.part_ml;
+  a.err = w.ctrl;
+  AttnArgs plan{};
+  plan.Hkv = d->Hkv;
+  plan.L_cap = d->L_cap;
+  plan.ctx_len = ctx_len;
+  plan.n_qtiles = g.n_qtiles;
+  plan.units = g.units;
+  plan.n_ctas = g.n_ctas;
+  plan.tile_start = w.tile_start;
+  plan.first_unit = w.first_unit;
+  plan.unit_ctas = w.unit_ctas;
+  plan.unit_done = w.unit_done;
+  plan.err = w.ctrl;
+  Q8_CUDA(cudaMemsetAsync(w.ctrl, 0, kCtrlBytes, st));
+  Q8_LAUNCH(TT_K_ATTN_PLAN, st, launch_attn_plan(plan, st));
   Q8_LAUNCH(TT_K_ATTN_Q8, st, launch_attn_q8(a, f->type, st));
+  Q8_LAUNCH(TT_K_MERGE_Q8, st, launch_attn_q8_merge(a, st));
   return TT_OK;
 }
 

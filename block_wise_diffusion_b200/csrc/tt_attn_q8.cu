@@ -1,7 +1,31 @@
-// Block-denoise attention over an 8-bit context cache, plain form: one CTA
-// per (sequence, KV head, 16 query rows) walks the keys 32 at a time with a
-// running maximum and sum in fp32.
-#include <cuda_fp16.h>
+// Block-denoise attention over an 8-bit context cache.
+//
+// Per query row, with s_j = q . k_j / sqrt(dh) (log2 units), v scale w_j and
+// codes c_j:  out = sum_j 2^(s_j) w_j c_j / sum_j 2^(s_j).
+// One pass: p_j = 2^(s_j + log2 w_j - m) with m a running maximum of s_j +
+// log2 w_j, O = sum p_j c_j, l = sum p_j / w_j, out = O / l.  The key scale
+// multiplies a score and the value scale adds log2 w_j to its exponent, both
+// per group of 16 keys, so neither costs an instruction per element; p_j <=
+// 2^8 whatever the scales, which lets P be fp16 (11 bits: its rounding is an
+// eighth of the output's).
+//
+// Both products run on the tensor cores in fp16 (kind::f16): every int8 and
+// e4m3 code is an fp16 number; a query row and the block's own bf16 keys and
+// values are brought into fp16 range by a power of two per row (per tile),
+// which is exact down to 2^-28 of the largest magnitude.
+//
+// Units, tiles and the balanced persistent schedule are those of the bf16
+// kernel (attn_plan_kernel).  Inside a CTA two chains run side by side, each
+// with 128 query rows, 128 TMEM columns of S / P and dh of O:
+//   S = Q . K(tile)^T -> softmax -> O += P . V(tile) -> next S ...
+// With more than 128 rows per KV head the chains take the two halves of the
+// rows and every tile; otherwise they share the rows and take every other
+// tile, so the tensor core works for one while the softmax runs for the other.
+// Roles (16 warps; registers are moved to the softmax by setmaxnreg):
+//   warps 0-3 / 4-7   softmax of chain 0 / 1, thread = row;
+//   warps 8-11        codes from global memory to registers, a tile ahead, to
+//                     fp16 in the swizzled K and V rings in shared memory;
+//   warps 12, 13      MMA issue of chain 0 / 1 (12 owns TMEM).
 #include <math.h>
 
 #include "tt_q8.h"
@@ -11,97 +35,685 @@ namespace tt {
 
 namespace {
 
-constexpr int kRows = 16, kKeys = 32, kThreads = 128;
+constexpr int kThreads = 512;
+constexpr int kConv = 128;                  // converter threads
+constexpr int kSlots = 2;                   // depth of the K and of the V ring
+constexpr uint32_t kSub = kAttnBN * 128;    // 128 rows x 64 fp16: 16 KB
+constexpr float kRescale = 8.0f;            // log2 units the running maximum may lag
+constexpr int kPCol = 64;                   // P starts at this column of S
+constexpr int kL2Ahead = 3;                 // tiles brought into L2 ahead of their load
 
-__device__ __forceinline__ float code_value(int type, uint8_t b) {
-  if (type == TT_Q8_INT8) return (float)(int8_t)b;
-  uint32_t h2;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"((uint16_t)b));
-  return __half2float(__ushort_as_half((unsigned short)(h2 & 0xFFFFu)));
+struct Smem {
+  uint32_t q, k, v, scales, bars, total;
+};
+__host__ __device__ constexpr Smem smem_layout(int dh) {
+  Smem s{};
+  const uint32_t nsub = (uint32_t)dh / 64;
+  s.q = 0;
+  s.k = s.q + 2 * nsub * kSub;
+  s.v = s.k + kSlots * nsub * kSub;
+  s.scales = s.v + kSlots * nsub * kSub;  // [slot][key scale, log2 w, 1 / w][8 groups]
+  s.bars = (s.scales + kSlots * 24 * 4 + 63) / 64 * 64;
+  s.total = s.bars + 256;
+  return s;
 }
 
-__global__ void __launch_bounds__(kThreads) attn_q8_kernel(const AttnQ8Args a, int type) {
+__device__ __forceinline__ uint8_t* align1024(uint8_t* p) {
+  return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
+}
+
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn_major) {
+  return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) |
+         ((uint32_t)(M >> 4) << 24);
+}
+
+// The CTA's range of the tile sequence, one unit's part at a time.
+struct Walk {
+  const int* start;
+  int t, hi, u;
+  __device__ __forceinline__ bool next(int& unit, int& a, int& b) {
+    if (t >= hi) return false;
+    const int s0 = start[u], s1 = start[u + 1];
+    unit = u++;
+    a = t - s0;
+    t = min(hi, s1);
+    b = t - s0;
+    return true;
+  }
+};
+
+struct Unit {
+  int b, g, qt, L;
+};
+__device__ __forceinline__ Unit unit_of(const AttnQ8Args& a, int u) {
+  Unit x;
+  const int pair = u / a.n_qtiles;
+  x.qt = u - pair * a.n_qtiles;
+  x.b = pair / a.Hkv;
+  x.g = pair - x.b * a.Hkv;
+  x.L = min(max(a.ctx_len[x.b], 0), a.L_cap);
+  return x;
+}
+// Valid keys of local tile t (0: the block's own keys).
+__device__ __forceinline__ int tile_keys(int t, int L, int S) {
+  return t == 0 ? S : min(kAttnBN, L - (t - 1) * kAttnBN);
+}
+
+// 2^e, e in [-126, 127]
+__device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
+
+// Exponent e with amax 2^-e in [2^14, 2^15), for the bf16 magnitude bits amax
+// (clamped so that 2^e and 2^-e are normal; 0 for zero and for non-finite).
+__device__ __forceinline__ int norm_exp(uint32_t amax) {
+  const int e = (int)(amax >> 7);
+  return e == 0 || e == 255 ? 0 : min(max(e - 127 - 14, -126), 126);
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// bf16 pair times a power of two, as an fp16 pair
+__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t w, float f) {
+  return pack_f16x2(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xFFFF0000u) * f);
+}
+
+// Four codes to two fp16 pairs.  int8: the byte with its sign bit flipped is
+// the code + 128, which as the low byte of 0x64xx makes 1024 + 128 + code.
+template <int TYPE>
+__device__ __forceinline__ void codes4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if constexpr (TYPE == TT_Q8_INT8) {
+    const uint32_t u = w ^ 0x80808080u;
+    asm("prmt.b32 %0, %2, %3, 0x4140;\n\tprmt.b32 %1, %2, %3, 0x4342;"
+        : "=r"(lo), "=r"(hi)
+        : "r"(u), "r"(0x64646464u));
+    asm("sub.f16x2 %0, %0, %1;" : "+r"(lo) : "r"(0x64806480u));
+    asm("sub.f16x2 %0, %0, %1;" : "+r"(hi) : "r"(0x64806480u));
+  } else {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+  }
+}
+
+__device__ __forceinline__ uint4 ldg_stream(const uint8_t* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+template <int N>
+__device__ __forceinline__ void reg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void reg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// Row `r` of a 128-byte-swizzled fp16 tile of dh columns: address of 16-byte
+// chunk c (8 values).
+__device__ __forceinline__ uint32_t chunk_at(int r, int c) {
+  return (uint32_t)(c >> 3) * kSub + (uint32_t)r * 128 + (uint32_t)(((c & 7) ^ (r & 7)) << 4);
+}
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                       uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+
+template <int TYPE, int DH>
+__global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a) {
   griddep_launch();
   griddep_wait();
-  __shared__ float sq[kRows][129], sk[kKeys][129], sv[kKeys][129], sp[kRows][kKeys + 1];
-  const int nrt = (a.S * a.G + kRows - 1) / kRows;
-  const int pair = blockIdx.x / nrt, rt = blockIdx.x - pair * nrt;
-  const int b = pair / a.Hkv, g = pair - b * a.Hkv;
-  int L = a.ctx_len[b];
-  if (L < 0 || L > a.L_cap) {
-    if (threadIdx.x == 0) atomicCAS(a.err, 0, (int)TT_ERR_INVALID_ARG);
-    L = min(max(L, 0), a.L_cap);
+  extern __shared__ uint8_t smem_raw[];
+  const int cta = blockIdx.x;
+  const long long T = a.tile_start[a.units];
+  const int lo = (int)((long long)cta * T / a.n_ctas);
+  const int hi = (int)((long long)(cta + 1) * T / a.n_ctas);
+  const int u0 = a.first_unit[cta];
+  if (lo >= hi) {
+    // An empty range lies inside the CTA range of at most one unit, the one
+    // that holds tile lo and starts before it: an empty record for the merge.
+    if (a.tile_start[u0] < lo)
+      for (int i = threadIdx.x; i < 256; i += kThreads)
+        *reinterpret_cast<float2*>(a.part_ml + ((size_t)(u0 + cta) * 256 + i) * 2) =
+            make_float2(-INFINITY, 0.f);
+    return;
   }
-  const int dh = a.dh, nrows = a.S * a.G;
-  for (int i = threadIdx.x; i < kRows * dh; i += kThreads) {
-    const int r = rt * kRows + i / dh, e = i % dh;
-    const int s = r / a.G, h = g * a.G + r % a.G;
-    sq[i / dh][e] =
-        r < nrows ? bf16_value(a.q[((long long)(b * a.S + s) * a.Hq + h) * dh + e]) : 0.f;
+  constexpr int NSUB = DH / 64;
+  constexpr Smem SL = smem_layout(DH);
+  uint8_t* base = align1024(smem_raw);
+  float* scales = reinterpret_cast<float*>(base + SL.scales);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(base + SL.bars);
+  uint64_t* q_full = bars;              // [chain] query rows written
+  uint64_t* s_full = q_full + 2;        // [chain] S ready, the P . V before it done
+  uint64_t* p_full = s_full + 2;        // [chain] P written, O corrected
+  uint64_t* o_full = p_full + 2;        // [chain] the segment's last P . V done
+  uint64_t* k_full = o_full + 2;        // [slot]
+  uint64_t* k_empty = k_full + kSlots;  // [slot]
+  uint64_t* v_full = k_empty + kSlots;
+  uint64_t* v_empty = v_full + kSlots;
+  uint64_t* sc_full = v_empty + kSlots;  // [slot]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sc_full + kSlots);
+  int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
+  uint32_t* red = tmem_slot + 2;  // [8] converter reduction
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool split = a.halves == 1;  // the chains share the rows and split the tiles
+  constexpr uint32_t kTmemCols = 2 * (kAttnBN + DH) <= 256 ? 256 : 512;
+  if (threadIdx.x == 0) {
+    const int users = split ? 1 : 2;  // chains that read a K / V slot
+    for (int c = 0; c < 2; ++c) {
+      mbar_init(&q_full[c], 128);
+      mbar_init(&s_full[c], 1);
+      mbar_init(&p_full[c], 128);
+      mbar_init(&o_full[c], 1);
+    }
+    for (int s = 0; s < kSlots; ++s) {
+      mbar_init(&k_full[s], kConv);
+      mbar_init(&k_empty[s], users);
+      mbar_init(&v_full[s], kConv);
+      mbar_init(&v_empty[s], users);
+      mbar_init(&sc_full[s], 8);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
   }
-  // thread = (row, every 8th column): 8 threads share a row
-  const int row = threadIdx.x >> 3, c8 = threadIdx.x & 7;
-  float o[16], m = -INFINITY, l = 0.f;
-  for (int i = 0; i < 16; ++i) o[i] = 0.f;
-  const long long crow = (long long)(b * a.Hkv + g) * a.L_cap;
-  for (int k0 = 0; k0 < a.S + L; k0 += kKeys) {
-    __syncthreads();
-    for (int i = threadIdx.x; i < kKeys * dh; i += kThreads) {
-      const int j = k0 + i / dh, e = i % dh;
-      float kv = 0.f, vv = 0.f;
-      if (j < a.S) {
-        const long long at = ((long long)(b * a.S + j) * a.Hkv + g) * dh + e;
-        kv = bf16_value(a.k_blk[at]);
-        vv = bf16_value(a.v_blk[at]);
-      } else if (j < a.S + L) {
-        const int p = j - a.S;
-        const long long at = (crow + p) * dh + e;
-        const long long sb = (long long)(b * a.Hkv + g) * a.n_blocks + p / a.block;
-        kv = code_value(type, a.k_ctx[at]) * a.k_scale[sb];
-        vv = code_value(type, a.v_ctx[at]) * a.v_scale[sb];
-      }
-      sk[i / dh][e] = kv;
-      sv[i / dh][e] = vv;
-    }
-    __syncthreads();
-    for (int j = c8; j < kKeys; j += 8) {
-      float s = -INFINITY;
-      if (k0 + j < a.S + L) {
-        s = 0.f;
-        for (int e = 0; e < dh; ++e) s = fmaf(sq[row][e], sk[j][e], s);
-        s *= a.scale_log2;
-      }
-      sp[row][j] = s;
-    }
-    __syncwarp();
-    float mn = m;
-    for (int j = 0; j < kKeys; ++j) mn = fmaxf(mn, sp[row][j]);
-    const float alpha = ex2(m - mn);
-    m = mn;
-    l *= alpha;
-    for (int i = 0; i < 16; ++i) o[i] *= alpha;
-    for (int j = 0; j < kKeys; ++j) {
-      const float p = ex2(sp[row][j] - m);
-      l += p;
+  if (warp == 12) {
+    tmem_alloc(tmem_slot, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  Walk walk{a.tile_start, lo, hi, u0};
+  int su, sa, sb;  // current segment: unit, local tiles [sa, sb)
+
+  if (warp < 8) {
+    // ------------------------------------------------------------ softmax
+    reg_inc<168>();
+    const int ch = warp >> 2;
+    const int r = threadIdx.x & 127;
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + ch * kAttnBN + lane_off;
+    const uint32_t tO = tmem + 2 * kAttnBN + ch * DH + lane_off;
+    const uint32_t sQ = smem_u32(base + SL.q) + ch * NSUB * kSub;
+    const bool valid = r < a.rows_per_half;
+    const bool busy = (warp & 3) * 32 < a.rows_per_half;  // the warp has a row
+    int kt = 0, pt = 0, qi = 0;                           // tiles of the CTA, turns, segments
+    bool ok = true;
+    for (; ok && walk.next(su, sa, sb); kt += sb - sa) {
+      const Unit un = unit_of(a, su);
+      const int slot = su + cta;
+      const int step = split ? 2 : 1, first = sa + (split ? ch : 0);
+      float m = -INFINITY, l = 0.f;
+      const int s_pos = un.qt * a.halves * a.s_per_half + (split ? 0 : ch * a.s_per_half) + r / a.G;
+      const int head = un.g * a.G + r % a.G;
+      const size_t qrow = (size_t)(un.b * a.S + s_pos) * a.Hq + head;
+      if (first < sb) {
+        // The query row, by a power of two in fp16 range.  The previous
+        // segment's last S of this chain has been waited for below.
+        float c_row = 0.f;
+        {
+          uint4 x[DH / 8];
+          uint32_t mx = 0;
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (i * 8 < dh) o[i] = fmaf(p, sv[j][i * 8 + c8], o[i]);
+          for (int i = 0; i < DH / 8; ++i)
+            x[i] = valid ? *reinterpret_cast<const uint4*>(a.q + qrow * DH + i * 8)
+                         : make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int i = 0; i < DH / 8; ++i) {
+            mx = __vmaxu2(mx, x[i].x & 0x7FFF7FFFu);
+            mx = __vmaxu2(mx, x[i].y & 0x7FFF7FFFu);
+            mx = __vmaxu2(mx, x[i].z & 0x7FFF7FFFu);
+            mx = __vmaxu2(mx, x[i].w & 0x7FFF7FFFu);
+          }
+          const int e = norm_exp(max(mx & 0xFFFFu, mx >> 16));
+          const float f = pow2i(-e);
+          c_row = a.scale_log2 * pow2i(e);
+#pragma unroll
+          for (int i = 0; i < DH / 8; ++i)
+            sts128(sQ + chunk_at(r, i), bf16x2_to_f16x2(x[i].x, f), bf16x2_to_f16x2(x[i].y, f),
+                   bf16x2_to_f16x2(x[i].z, f), bf16x2_to_f16x2(x[i].w, f));
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(&q_full[ch]);
+
+        for (int i = first; i < sb; i += step, ++pt) {
+          const int t = kt + i - sa, ts = split ? ch : t & 1;
+          if (!mbar_wait_inline(&sc_full[ts], (uint32_t)(split ? pt : t >> 1) & 1u, a.err, abort_flag, WHERE_ATTN_SOFTMAX) ||
+              !mbar_wait_inline(&s_full[ch], (uint32_t)pt & 1u, a.err, abort_flag, WHERE_ATTN_SOFTMAX)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          if (busy) {
+            // Two passes over the 128 scores, 32 at a time: the maximum, then the
+            // exponentials.  The second pass finds columns 64.. still in
+            // registers and reads 0..63 again meanwhile; P goes over columns
+            // 64..127, whose scores nobody needs any more.
+            const float* sc = scales + ts * 24;
+            const int nv = tile_keys(i, un.L, a.S);
+            float mx = -INFINITY;
+            uint32_t x0[32], x2[32], x3[32];
+            auto maxes = [&](uint32_t(&x)[32], int k) {
+              if (nv < kAttnBN) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                  if (32 * k + j >= nv) x[j] = __float_as_uint(-INFINITY);
+              }
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                float y = fmaxf(__uint_as_float(x[16 * h]), __uint_as_float(x[16 * h + 1]));
+#pragma unroll
+                for (int j = 2; j < 16; j += 2)
+                  y = fmax3(y, __uint_as_float(x[16 * h + j]), __uint_as_float(x[16 * h + j + 1]));
+                mx = fmaxf(mx, fmaf(y, c_row * sc[2 * k + h], sc[8 + 2 * k + h]));
+              }
+            };
+            auto exps = [&](uint32_t(&x)[32], int k) {
+              if (k < 2 && nv < kAttnBN) {  // read again: without the mask
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                  if (32 * k + j >= nv) x[j] = __float_as_uint(-INFINITY);
+              }
+              uint32_t p[16];
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const float cg = c_row * sc[2 * k + h], off = sc[8 + 2 * k + h] - m;
+                float e0 = 0.f, e1 = 0.f;
+#pragma unroll
+                for (int j = 0; j < 16; j += 2) {
+                  const float p0 = ex2(fmaf(__uint_as_float(x[16 * h + j]), cg, off));
+                  const float p1 = ex2(fmaf(__uint_as_float(x[16 * h + j + 1]), cg, off));
+                  e0 += p0;
+                  e1 += p1;
+                  p[8 * h + (j >> 1)] = pack_f16x2(p0, p1);
+                }
+                l = fmaf(e0 + e1, sc[16 + 2 * k + h], l);
+              }
+              tmem_st16(tS + kPCol + 16 * k, p);
+            };
+            tmem_ld32(tS, x0);
+            tmem_wait_ld();
+            tmem_ld32(tS + 64, x2);
+            maxes(x0, 0);
+            tmem_wait_ld();
+            tmem_ld32(tS + 32, x0);
+            maxes(x2, 2);
+            tmem_wait_ld();
+            tmem_ld32(tS + 96, x3);
+            maxes(x0, 1);
+            tmem_wait_ld();
+            tmem_ld32(tS, x0);
+            maxes(x3, 3);
+            const bool need = mx > m + kRescale;
+            float alpha = 1.f;
+            if (need) {
+              alpha = ex2(m - mx);
+              m = mx;
+            }
+            l *= alpha;
+            exps(x2, 2);
+            tmem_wait_ld();
+            tmem_ld32(tS + 32, x2);
+            exps(x3, 3);
+            exps(x0, 0);
+            tmem_wait_ld();
+            exps(x2, 1);
+            // O to the new maximum before P . V adds to it; a segment's first
+            // P . V overwrites O
+            if (i > first && __any_sync(0xffffffffu, need)) {
+#pragma unroll 1
+              for (int c0 = 0; c0 < DH; c0 += 32) {
+                tmem_ld32(tO + c0, x0);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                  x0[j] = __float_as_uint(__uint_as_float(x0[j]) * alpha);
+                tmem_st32(tO + c0, x0);
+              }
+            }
+            tmem_wait_st();
+          }
+          tc_fence_before();
+          mbar_arrive(&p_full[ch]);
+        }
+        if (!ok) break;
+        if (!mbar_wait_inline(&o_full[ch], (uint32_t)qi & 1u, a.err, abort_flag, WHERE_ATTN_SOFTMAX)) {
+          ok = false;
+          break;
+        }
+        ++qi;
+        tc_fence_after();
+      }
+      // The segment's partial: unnormalised O (tile-major [slot][dh/4][256
+      // rows][4], a warp's store is 512 contiguous bytes) and (m, l).
+      const int r256 = ch * 128 + r;
+      if (busy && first < sb) {
+        float* po = a.part_o + (size_t)slot * DH * 256 + (size_t)r256 * 4;
+#pragma unroll 1
+        for (int c0 = 0; c0 < DH; c0 += 32) {
+          uint32_t o[32];
+          tmem_ld32(tO + c0, o);
+          tmem_wait_ld();
+          if (valid) {
+#pragma unroll
+            for (int v = 0; v < 8; ++v)
+              *reinterpret_cast<float4*>(po + (size_t)(c0 / 4 + v) * 1024) =
+                  make_float4(__uint_as_float(o[4 * v]), __uint_as_float(o[4 * v + 1]),
+                              __uint_as_float(o[4 * v + 2]), __uint_as_float(o[4 * v + 3]));
+          }
+        }
+      }
+      if (valid)
+        *reinterpret_cast<float2*>(a.part_ml + ((size_t)slot * 256 + r256) * 2) =
+            make_float2(m, l);
+    }
+  } else if (warp < 12) {
+    // ---------------------------------------------- codes to fp16 tiles
+    reg_dec<120>();
+    const int tid = threadIdx.x - 256;
+    constexpr int NV = kAttnBN * DH / 16 / kConv;  // 16-code chunks per thread
+    constexpr int CPR = DH / 16;                   // chunks per row
+    const int row0 = tid / CPR, col = tid % CPR;   // chunk i: row row0 + i * kConv / CPR
+    const uint32_t sK = smem_u32(base + SL.k), sV = smem_u32(base + SL.v);
+    uint4 kr[NV], vr[NV];
+    float nk = 1.f, nw = 1.f;  // next tile's scales of group tid (tid < 8)
+    auto load = [&](uint4 (&x)[NV], const uint8_t* p, int nv) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int row = row0 + i * (kConv / CPR);
+        x[i] = row < nv ? ldg_stream(p + (size_t)row * DH + col * 16) : make_uint4(0, 0, 0, 0);
+      }
+    };
+    // Chunk i of the registers as 32 bytes of fp16.  Columns 64.. store their
+    // two 16-byte halves in the other order: eight lanes of a store then hit
+    // eight different bank groups.
+    auto store = [&](const uint4 (&x)[NV], uint32_t dst) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int row = row0 + i * (kConv / CPR);
+        uint32_t w[8];
+        codes4<TYPE>(x[i].x, w[0], w[1]);
+        codes4<TYPE>(x[i].y, w[2], w[3]);
+        codes4<TYPE>(x[i].z, w[4], w[5]);
+        codes4<TYPE>(x[i].w, w[6], w[7]);
+        const bool odd = col >= 4;
+        const uint32_t a0 = dst + chunk_at(row, 2 * col), a1 = dst + chunk_at(row, 2 * col + 1);
+        sts128(odd ? a1 : a0, odd ? w[4] : w[0], odd ? w[5] : w[1], odd ? w[6] : w[2],
+               odd ? w[7] : w[3]);
+        sts128(odd ? a0 : a1, odd ? w[0] : w[4], odd ? w[1] : w[5], odd ? w[2] : w[6],
+               odd ? w[3] : w[7]);
+      }
+    };
+    // The block's own rows [S, Hkv, dh] (bf16) by a power of two in fp16
+    // range; returns its exponent.  Rows past S are zero.
+    auto block_rows = [&](const uint16_t* p, uint32_t dst, int slot_id) -> int {
+      constexpr int NB = kAttnBN * DH / 8 / kConv;
+      uint32_t mx = 0;
+      const int c0 = tid % (DH / 8), r0 = tid / (DH / 8);
+#pragma unroll 4
+      for (int i = 0; i < NB; ++i) {
+        const int row = r0 + i * (kConv / (DH / 8));
+        if (row < a.S) {
+          const uint4 x = *reinterpret_cast<const uint4*>(p + (size_t)row * a.Hkv * DH + c0 * 8);
+          mx = __vmaxu2(mx, x.x & 0x7FFF7FFFu);
+          mx = __vmaxu2(mx, x.y & 0x7FFF7FFFu);
+          mx = __vmaxu2(mx, x.z & 0x7FFF7FFFu);
+          mx = __vmaxu2(mx, x.w & 0x7FFF7FFFu);
+        }
+      }
+      mx = __reduce_max_sync(0xffffffffu, max(mx & 0xFFFFu, mx >> 16));
+      named_bar_sync(1, kConv);  // the previous use of red is over
+      if (lane == 0) red[(warp - 8) + 4 * slot_id] = mx;
+      named_bar_sync(1, kConv);
+      const uint32_t* rd = red + 4 * slot_id;
+      const int e = norm_exp(max(max(rd[0], rd[1]), max(rd[2], rd[3])));
+      const float f = pow2i(-e);
+#pragma unroll 4
+      for (int i = 0; i < NB; ++i) {
+        const int row = r0 + i * (kConv / (DH / 8));
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (row < a.S)
+          x = *reinterpret_cast<const uint4*>(p + (size_t)row * a.Hkv * DH + c0 * 8);
+        sts128(dst + chunk_at(row, c0), bf16x2_to_f16x2(x.x, f), bf16x2_to_f16x2(x.y, f),
+               bf16x2_to_f16x2(x.z, f), bf16x2_to_f16x2(x.w, f));
+      }
+      return e;
+    };
+    int kt = 0, used0 = 0, used1 = 0;  // tiles, uses of each slot
+    bool ok = true;
+    bool have = false;  // the registers hold the tile about to be stored
+    while (ok && walk.next(su, sa, sb)) {
+      const Unit un = unit_of(a, su);
+      const size_t pair = (size_t)un.b * a.Hkv + un.g;
+      const uint8_t* kp = a.k_ctx + pair * a.L_cap * DH;
+      const uint8_t* vp = a.v_ctx + pair * a.L_cap * DH;
+      const float* ksp = a.k_scale + pair * a.n_blocks;
+      const float* vsp = a.v_scale + pair * a.n_blocks;
+      auto load_scales = [&](int tl) {
+        if (tid < 8) {
+          const int pos = (tl - 1) * kAttnBN + tid * 16;
+          nk = pos < un.L ? __ldg(ksp + pos / a.block) : 1.f;
+          nw = pos < un.L ? __ldg(vsp + pos / a.block) : 1.f;
+        }
+      };
+      have = false;
+      for (int tl = sa; tl < sb; ++tl, ++kt) {
+        // the ring: slots by turns, or one slot per chain (each barrier then
+        // has one reader that sees its phases in order)
+        const int slot = split ? (tl - sa) & 1 : kt & 1;
+        const uint32_t par = ((uint32_t)(slot ? used1++ : used0++) & 1u) ^ 1u;
+        const uint32_t dK = sK + slot * NSUB * kSub, dV = sV + slot * NSUB * kSub;
+        const bool more = tl + 1 < sb;
+        const size_t key0 = (size_t)(max(tl, 1) - 1) * kAttnBN;
+        if (tl > 0 && !have) {
+          load(kr, kp + key0 * DH, tile_keys(tl, un.L, a.S));
+          load(vr, vp + key0 * DH, tile_keys(tl, un.L, a.S));
+          load_scales(tl);
+        }
+        if (tid == 0 && tl + kL2Ahead < sb) {
+          const size_t at = (size_t)(tl + kL2Ahead - 1) * kAttnBN * DH;
+          const uint32_t n = (uint32_t)tile_keys(tl + kL2Ahead, un.L, a.S) * DH;
+          prefetch_l2_bulk(kp + at, n);
+          prefetch_l2_bulk(vp + at, n);
+        }
+        if (!mbar_wait_inline(&k_empty[slot], par, a.err, abort_flag, WHERE_ATTN_PRODUCER)) {
+          ok = false;
+          break;
+        }
+        int ek = 0, ev = 0;
+        if (tl == 0)
+          ek = block_rows(a.k_blk + ((size_t)un.b * a.S * a.Hkv + un.g) * DH, dK, 0);
+        else
+          store(kr, dK);
+        fence_proxy_async_smem();
+        mbar_arrive(&k_full[slot]);
+        if (more)
+          load(kr, kp + (size_t)tl * kAttnBN * DH, tile_keys(tl + 1, un.L, a.S));
+        if (!mbar_wait_inline(&v_empty[slot], par, a.err, abort_flag, WHERE_ATTN_PRODUCER)) {
+          ok = false;
+          break;
+        }
+        // The scales go with V: once P . V of the tile that had the slot
+        // before has run, the softmax is done with that tile's scales.
+        if (tl == 0) ev = block_rows(a.v_blk + ((size_t)un.b * a.S * a.Hkv + un.g) * DH, dV, 1);
+        if (tid < 8) {
+          float* sc = scales + slot * 24;
+          const float w = tl == 0 ? pow2i(ev) : nw;
+          sc[tid] = tl == 0 ? pow2i(ek) : nk;
+          sc[8 + tid] = tl == 0 ? (float)ev : log2f(w);
+          sc[16 + tid] = 1.f / w;
+          mbar_arrive(&sc_full[slot]);
+        }
+        if (tl > 0) store(vr, dV);
+        fence_proxy_async_smem();
+        mbar_arrive(&v_full[slot]);
+        if (more) {
+          load(vr, vp + (size_t)tl * kAttnBN * DH, tile_keys(tl + 1, un.L, a.S));
+          load_scales(tl + 1);
+        }
+        have = more;
+      }
+    }
+  } else {
+    // ---------------------------------------------------------- MMA issue
+    reg_dec<56>();
+    const int ch = warp - 12;
+    if (ch < 2) {
+      constexpr uint32_t idS = idesc_f16(128, kAttnBN, false), idO = idesc_f16(128, DH, true);
+      const uint32_t tS = tmem + ch * kAttnBN, tO = tmem + 2 * kAttnBN + ch * DH;
+      const uint64_t dQ = sdesc_sw128(smem_u32(base + SL.q) + ch * NSUB * kSub, 16, 1024);
+      const uint64_t dK0 = sdesc_sw128(smem_u32(base + SL.k), 16, 1024);
+      const uint64_t dV0 = sdesc_sw128(smem_u32(base + SL.v), kSub, 1024);
+      int kt = 0, pt = 0, qi = 0;
+      bool ok = true;
+      for (; ok && walk.next(su, sa, sb); kt += sb - sa) {
+        const int L = unit_of(a, su).L;
+        const int step = split ? 2 : 1, first = sa + (split ? ch : 0);
+        if (first >= sb) continue;
+        auto scores = [&](int i, int turn) -> bool {
+          const int t = kt + i - sa, slot = split ? ch : t & 1;
+          if (!mbar_wait_inline(&k_full[slot], (uint32_t)(split ? turn : t >> 1) & 1u, a.err,
+                                abort_flag, WHERE_ATTN_MMA))
+            return false;
+          tc_fence_after();
+          if (lane == 0) {
+            const uint64_t dK = dK0 + (uint64_t)((uint32_t)(slot * NSUB) * (kSub >> 4));
+#pragma unroll
+            for (int k = 0; k < DH / 16; ++k) {
+              const uint64_t off = (uint64_t)(((k >> 2) * kSub + (k & 3) * 32) >> 4);
+              umma_bf16_ss(tS, dQ + off, dK + off, idS, k > 0);
+            }
+            umma_commit(&s_full[ch]);
+            umma_commit(&k_empty[slot]);
+          }
+          __syncwarp();
+          return true;
+        };
+        ok = mbar_wait_inline(&q_full[ch], (uint32_t)qi & 1u, a.err, abort_flag, WHERE_ATTN_MMA);
+        if (ok) tc_fence_after();
+        if (ok) ok = scores(first, pt);
+        for (int i = first; ok && i < sb; i += step, ++pt) {
+          const int t = kt + i - sa, slot = split ? ch : t & 1;
+          if (!mbar_wait_inline(&p_full[ch], (uint32_t)pt & 1u, a.err, abort_flag, WHERE_ATTN_MMA) ||
+              !mbar_wait_inline(&v_full[slot], (uint32_t)(split ? pt : t >> 1) & 1u, a.err, abort_flag,
+                         WHERE_ATTN_MMA)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          if (lane == 0) {
+            const int ksteps = (tile_keys(i, L, a.S) + 15) >> 4;
+            const uint64_t dV = dV0 + (uint64_t)((uint32_t)(slot * NSUB) * (kSub >> 4));
+#pragma unroll
+            for (int k = 0; k < kAttnBN / 16; ++k)
+              if (k < ksteps)
+                umma_bf16_ts(tO, tS + kPCol + k * 8, dV + (uint64_t)(k * (2048 >> 4)), idO,
+                             (i > first || k > 0) ? 1u : 0u);
+            umma_commit(&v_empty[slot]);
+            if (i + step >= sb) umma_commit(&o_full[ch]);
+          }
+          __syncwarp();
+          if (i + step < sb) ok = scores(i + step, pt + 1);
+        }
+        ++qi;
+      }
     }
   }
-  const int r = rt * kRows + row;
-  if (r >= nrows) return;
-  const int s = r / a.G, h = g * a.G + r % a.G;
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 12) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// Thread = (unit, query row, 4 columns): the unit's segment partials (two per
+// segment where the chains split the tiles) into the bf16 output, in one
+// pass with a running maximum.
+__global__ void __launch_bounds__(256) attn_q8_merge_kernel(const AttnQ8Args a) {
+  griddep_launch();
+  griddep_wait();
+  const int ngrp = a.dh / 4, rows = a.halves * 128;
+  const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+  const int row = (int)(i % rows);
+  const int grp = (int)(i / rows % ngrp);
+  const long long u = i / rows / ngrp;
+  if (u >= a.units) return;
+  const int h = row >> 7, r = row & 127;
+  if (r >= a.rows_per_half) return;
+  const int4 uc = a.unit_ctas[u];
+  const int per = a.halves == 1 ? 2 : 1;  // partials per segment
+  const int n = (uc.y - uc.x + 1) * per;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float den = 0.f, mrun = -INFINITY;
+  for (int c0 = 0; c0 < n; c0 += 4) {
+    float2 ml[4];
+    float4 o[4];
 #pragma unroll
-  for (int i = 0; i < 16; ++i)
-    if (i * 8 < dh)
-      a.out[((long long)(b * a.S + s) * a.Hq + h) * dh + i * 8 + c8] = bf16_bits(o[i] / l);
+    for (int k = 0; k < 4; ++k) {
+      const int c = c0 + k;
+      const size_t slot = (size_t)u + uc.x + c / per;
+      const size_t at = per == 2 ? (size_t)((c & 1) * 128 + r) : (size_t)row;
+      ml[k] = c < n ? __ldcg(reinterpret_cast<const float2*>(a.part_ml + (slot * 256 + at) * 2))
+                    : make_float2(-INFINITY, 0.f);
+      o[k] = c < n ? __ldcg(reinterpret_cast<const float4*>(a.part_o + ((slot * ngrp + grp) * 256 + at) * 4))
+                   : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (ml[k].y == 0.f) continue;  // no keys: its O was never written
+      const float mn = ml[k].x > mrun ? ml[k].x : mrun;
+      const float w0 = ex2(mrun - mn), w1 = ex2(ml[k].x - mn);
+      mrun = mn;
+      den = fmaf(den, w0, ml[k].y * w1);
+      acc.x = fmaf(acc.x, w0, o[k].x * w1);
+      acc.y = fmaf(acc.y, w0, o[k].y * w1);
+      acc.z = fmaf(acc.z, w0, o[k].z * w1);
+      acc.w = fmaf(acc.w, w0, o[k].w * w1);
+    }
+  }
+  const float inv = 1.f / den;
+  const int qt = (int)(u % a.n_qtiles);
+  const long long pair = u / a.n_qtiles;
+  const long long b = pair / a.Hkv, g = pair % a.Hkv;
+  const int s = qt * a.halves * a.s_per_half + h * a.s_per_half + r / a.G;
+  const int head = (int)g * a.G + r % a.G;
+  *reinterpret_cast<uint2*>(a.out + ((size_t)(b * a.S + s) * a.Hq + head) * a.dh + grp * 4) =
+      make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+}
+
+template <int TYPE, int DH>
+cudaError_t launch_main(const AttnQ8Args& a, cudaStream_t st) {
+  constexpr size_t smem = smem_layout(DH).total + 1024;
+  static_assert(smem <= 232448, "shared memory per CTA");
+  cudaError_t e = cudaFuncSetAttribute(attn_q8_kernel<TYPE, DH>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  return launch_k(attn_q8_kernel<TYPE, DH>, dim3(a.n_ctas), dim3(kThreads), smem, st, a);
 }
 
 }  // namespace
 
 cudaError_t launch_attn_q8(const AttnQ8Args& a, int type, cudaStream_t st) {
-  const int nrt = (a.S * a.G + kRows - 1) / kRows;
-  return launch_k(attn_q8_kernel, dim3(a.B * a.Hkv * nrt), dim3(kThreads), 0, st, a, type);
+  if (type == TT_Q8_INT8)
+    return a.dh == 64 ? launch_main<TT_Q8_INT8, 64>(a, st) : launch_main<TT_Q8_INT8, 128>(a, st);
+  return a.dh == 64 ? launch_main<TT_Q8_E4M3, 64>(a, st) : launch_main<TT_Q8_E4M3, 128>(a, st);
+}
+
+cudaError_t launch_attn_q8_merge(const AttnQ8Args& a, cudaStream_t st) {
+  const long long threads = (long long)a.units * a.halves * 128 * (a.dh / 4);
+  return launch_k(attn_q8_merge_kernel, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, st,
+                  a);
 }
 
 }  // namespace tt

@@ -62,9 +62,9 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
 
 // Bounded wait for the phase with the given parity.  `abort_flag` is a CTA
 // shared word: once any thread has timed out, later waits return at once.
-static __device__ __noinline__ bool mbar_wait_slow(uint64_t* bar, uint32_t parity, int* err,
-                                                   volatile int* abort_flag, int where,
-                                                   uint64_t limit_ns = kWaitLimitNs) {
+__device__ __forceinline__ bool mbar_wait_inline(uint64_t* bar, uint32_t parity, int* err,
+                                                 volatile int* abort_flag, int where,
+                                                 uint64_t limit_ns = kWaitLimitNs) {
   const uint64_t t0 = global_ns();
   for (uint32_t i = 0;; ++i) {
     // A completed phase wins over the abort flag, so threads waiting on the
@@ -80,6 +80,13 @@ static __device__ __noinline__ bool mbar_wait_slow(uint64_t* bar, uint32_t parit
       return false;
     }
   }
+}
+// The same as a call; kernels that move registers between their warps
+// (setmaxnreg) cannot make calls and use the inline form.
+static __device__ __noinline__ bool mbar_wait_slow(uint64_t* bar, uint32_t parity, int* err,
+                                                   volatile int* abort_flag, int where,
+                                                   uint64_t limit_ns = kWaitLimitNs) {
+  return mbar_wait_inline(bar, parity, err, abort_flag, where, limit_ns);
 }
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int* err,
                                           volatile int* abort_flag, int where) {

@@ -45,6 +45,7 @@ cudaError_t launch_gemm_i8_linear(const CUtensorMap& tmA, const CUtensorMap& tmB
                                   const GemmI8Args& a, int grid, cudaStream_t st);
 
 // --------------------------------------------------------------- attention
+// Units, tiles and CTA ranges as AttnArgs describes them.
 struct AttnQ8Args {
   int B, S, Hq, Hkv, dh, G, L_cap, block, n_blocks;
   const uint16_t *q, *k_blk, *v_blk;
@@ -53,9 +54,22 @@ struct AttnQ8Args {
   const int* ctx_len;
   float scale_log2;  // log2(e) / sqrt(dh)
   uint16_t* out;
+  int s_per_half, rows_per_half, halves, n_qtiles, units, n_ctas;
+  const int* tile_start;   // the plan: [units + 1], [n_ctas], [units]
+  const int* first_unit;
+  const int4* unit_ctas;
+  float* part_o;   // [units + n_ctas - 1][dh/4][256][4] unnormalised outputs
+  float* part_ml;  // [units + n_ctas - 1][256][2]: maximum (log2 units), sum
   int* err;
 };
 cudaError_t launch_attn_q8(const AttnQ8Args& a, int type, cudaStream_t st);
+cudaError_t launch_attn_q8_merge(const AttnQ8Args& a, cudaStream_t st);
+
+// Query packing and CTA count of an attention call, as the bf16 call has them.
+struct AttnShape {
+  int G, s_per_half, rows_per_half, halves, n_qtiles, units, n_ctas;
+};
+AttnShape attn_shape(const tt_dims& d);
 
 // Workspace bytes of the 8-bit calls of tt_workspace_bytes (d already checked).
 size_t q8_workspace_bytes(const tt_dims& d, int which);
