@@ -23,9 +23,10 @@
 // tile, so the tensor core works for one while the softmax runs for the other.
 // Roles (16 warps; registers are moved to the softmax by setmaxnreg):
 //   warps 0-3 / 4-7   softmax of chain 0 / 1, thread = row;
-//   warps 8-11        codes from global memory to registers, a tile ahead, to
-//                     fp16 in the swizzled K and V rings in shared memory;
-//   warps 12, 13      MMA issue of chain 0 / 1 (12 owns TMEM).
+//   warps 8-11        codes of one tile in shared memory to fp16 in the swizzled
+//                     K and V rings;
+//   warps 12, 13      MMA issue of chain 0 / 1 (12 owns TMEM);
+//   warp 14           codes from global to shared memory.
 #include <math.h>
 
 #include "tt_q8.h"
@@ -40,11 +41,10 @@ constexpr int kConv = 128;                  // converter threads
 constexpr int kSlots = 2;                   // depth of the K and of the V ring
 constexpr uint32_t kSub = kAttnBN * 128;    // 128 rows x 64 fp16: 16 KB
 constexpr float kRescale = 8.0f;            // log2 units the running maximum may lag
-constexpr int kPCol = 64;                   // P starts at this column of S
 constexpr int kL2Ahead = 3;                 // tiles brought into L2 ahead of their load
 
 struct Smem {
-  uint32_t q, k, v, scales, bars, total;
+  uint32_t q, k, v, raw, scales, bars, total;
 };
 __host__ __device__ constexpr Smem smem_layout(int dh) {
   Smem s{};
@@ -52,7 +52,8 @@ __host__ __device__ constexpr Smem smem_layout(int dh) {
   s.q = 0;
   s.k = s.q + 2 * nsub * kSub;
   s.v = s.k + kSlots * nsub * kSub;
-  s.scales = s.v + kSlots * nsub * kSub;  // [slot][key scale, log2 w, 1 / w][8 groups]
+  s.raw = s.v + kSlots * nsub * kSub;    // codes of one K and one V tile
+  s.scales = s.raw + 2 * kAttnBN * dh;  // [slot][key scale, log2 w, 1 / w][8 groups]
   s.bars = (s.scales + kSlots * 24 * 4 + 63) / 64 * 64;
   s.total = s.bars + 256;
   return s;
@@ -138,11 +139,57 @@ __device__ __forceinline__ void codes4(uint32_t w, uint32_t& lo, uint32_t& hi) {
   }
 }
 
-__device__ __forceinline__ uint4 ldg_stream(const uint8_t* p) {
+// Pairs of fp32 in one 64-bit register: one instruction for two.
+__device__ __forceinline__ uint64_t pack2u(uint32_t x, uint32_t y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(x), "r"(y));
+  return r;
+}
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+  return pack2u(__float_as_uint(x), __float_as_uint(y));
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// TMEM, 8 columns of the thread's lane.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                 "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+               "r"(r[7])
+               : "memory");
+}
+
+// `bytes` (a multiple of 16) from global to shared memory, counted on `bar`.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          dst),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
+               : "r"(addr));
   return v;
 }
 
@@ -199,7 +246,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
   uint64_t* v_full = k_empty + kSlots;
   uint64_t* v_empty = v_full + kSlots;
   uint64_t* sc_full = v_empty + kSlots;  // [slot]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sc_full + kSlots);
+  uint64_t* rk_full = sc_full + kSlots;  // [K, V] a tile of codes has landed
+  uint64_t* rk_empty = rk_full + 2;      // [K, V] it has been converted
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(rk_empty + 2);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
   uint32_t* red = tmem_slot + 2;  // [8] converter reduction
 
@@ -213,6 +262,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
       mbar_init(&s_full[c], 1);
       mbar_init(&p_full[c], 128);
       mbar_init(&o_full[c], 1);
+      mbar_init(&rk_full[c], 1);
+      mbar_init(&rk_empty[c], kConv);
     }
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(&k_full[s], kConv);
@@ -237,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
 
   if (warp < 8) {
     // ------------------------------------------------------------ softmax
-    reg_inc<168>();
+    reg_inc<192>();
     const int ch = warp >> 2;
     const int r = threadIdx.x & 127;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
@@ -287,98 +338,93 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
 
         for (int i = first; i < sb; i += step, ++pt) {
           const int t = kt + i - sa, ts = split ? ch : t & 1;
-          if (!mbar_wait_inline(&sc_full[ts], (uint32_t)(split ? pt : t >> 1) & 1u, a.err, abort_flag, WHERE_ATTN_SOFTMAX) ||
-              !mbar_wait_inline(&s_full[ch], (uint32_t)pt & 1u, a.err, abort_flag, WHERE_ATTN_SOFTMAX)) {
+          if (!mbar_wait_inline(&sc_full[ts], (uint32_t)(split ? pt : t >> 1) & 1u, a.err,
+                                abort_flag, WHERE_ATTN_SOFTMAX)) {
+            ok = false;
+            break;
+          }
+          float cg[8], lw[8], iw[8];  // per 16 keys: score factor, log2 w, 1 / w
+#pragma unroll
+          for (int g = 0; g < 8; g += 4) {
+            const float4* sc = reinterpret_cast<const float4*>(scales + ts * 24 + g);
+            const float4 x = sc[0], y = sc[2], z = sc[4];
+            cg[g] = c_row * x.x, cg[g + 1] = c_row * x.y;
+            cg[g + 2] = c_row * x.z, cg[g + 3] = c_row * x.w;
+            lw[g] = y.x, lw[g + 1] = y.y, lw[g + 2] = y.z, lw[g + 3] = y.w;
+            iw[g] = z.x, iw[g + 1] = z.y, iw[g + 2] = z.z, iw[g + 3] = z.w;
+          }
+          if (!mbar_wait_inline(&s_full[ch], (uint32_t)pt & 1u, a.err, abort_flag,
+                                WHERE_ATTN_SOFTMAX)) {
             ok = false;
             break;
           }
           tc_fence_after();
           if (busy) {
-            // Two passes over the 128 scores, 32 at a time: the maximum, then the
-            // exponentials.  The second pass finds columns 64.. still in
-            // registers and reads 0..63 again meanwhile; P goes over columns
-            // 64..127, whose scores nobody needs any more.
-            const float* sc = scales + ts * 24;
+            uint32_t s[128];
+            tmem_ld32(tS, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
+            tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
+            tmem_ld32(tS + 64, *reinterpret_cast<uint32_t(*)[32]>(&s[64]));
+            tmem_ld32(tS + 96, *reinterpret_cast<uint32_t(*)[32]>(&s[96]));
+            tmem_wait_ld();
             const int nv = tile_keys(i, un.L, a.S);
-            float mx = -INFINITY;
-            uint32_t x0[32], x2[32], x3[32];
-            auto maxes = [&](uint32_t(&x)[32], int k) {
-              if (nv < kAttnBN) {
+            if (nv < kAttnBN) {
 #pragma unroll
-                for (int j = 0; j < 32; ++j)
-                  if (32 * k + j >= nv) x[j] = __float_as_uint(-INFINITY);
+              for (int j = 0; j < 128; ++j)
+                if (j >= nv) s[j] = __float_as_uint(-INFINITY);
+            }
+            float gm[8];
+#pragma unroll
+            for (int g = 0; g < 8; ++g) {
+              const uint32_t* x = s + 16 * g;
+              float y0 = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
+              float y1 = fmaxf(__uint_as_float(x[2]), __uint_as_float(x[3]));
+#pragma unroll
+              for (int j = 4; j < 16; j += 4) {
+                y0 = fmax3(y0, __uint_as_float(x[j]), __uint_as_float(x[j + 1]));
+                y1 = fmax3(y1, __uint_as_float(x[j + 2]), __uint_as_float(x[j + 3]));
               }
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                float y = fmaxf(__uint_as_float(x[16 * h]), __uint_as_float(x[16 * h + 1]));
-#pragma unroll
-                for (int j = 2; j < 16; j += 2)
-                  y = fmax3(y, __uint_as_float(x[16 * h + j]), __uint_as_float(x[16 * h + j + 1]));
-                mx = fmaxf(mx, fmaf(y, c_row * sc[2 * k + h], sc[8 + 2 * k + h]));
-              }
-            };
-            auto exps = [&](uint32_t(&x)[32], int k) {
-              if (k < 2 && nv < kAttnBN) {  // read again: without the mask
-#pragma unroll
-                for (int j = 0; j < 32; ++j)
-                  if (32 * k + j >= nv) x[j] = __float_as_uint(-INFINITY);
-              }
-              uint32_t p[16];
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const float cg = c_row * sc[2 * k + h], off = sc[8 + 2 * k + h] - m;
-                float e0 = 0.f, e1 = 0.f;
-#pragma unroll
-                for (int j = 0; j < 16; j += 2) {
-                  const float p0 = ex2(fmaf(__uint_as_float(x[16 * h + j]), cg, off));
-                  const float p1 = ex2(fmaf(__uint_as_float(x[16 * h + j + 1]), cg, off));
-                  e0 += p0;
-                  e1 += p1;
-                  p[8 * h + (j >> 1)] = pack_f16x2(p0, p1);
-                }
-                l = fmaf(e0 + e1, sc[16 + 2 * k + h], l);
-              }
-              tmem_st16(tS + kPCol + 16 * k, p);
-            };
-            tmem_ld32(tS, x0);
-            tmem_wait_ld();
-            tmem_ld32(tS + 64, x2);
-            maxes(x0, 0);
-            tmem_wait_ld();
-            tmem_ld32(tS + 32, x0);
-            maxes(x2, 2);
-            tmem_wait_ld();
-            tmem_ld32(tS + 96, x3);
-            maxes(x0, 1);
-            tmem_wait_ld();
-            tmem_ld32(tS, x0);
-            maxes(x3, 3);
+              gm[g] = fmaf(fmaxf(y0, y1), cg[g], lw[g]);
+            }
+            const float mx = fmaxf(fmax3(fmax3(gm[0], gm[1], gm[2]), gm[3], gm[4]),
+                                   fmax3(gm[5], gm[6], gm[7]));
             const bool need = mx > m + kRescale;
             float alpha = 1.f;
             if (need) {
               alpha = ex2(m - mx);
               m = mx;
             }
-            l *= alpha;
-            exps(x2, 2);
-            tmem_wait_ld();
-            tmem_ld32(tS + 32, x2);
-            exps(x3, 3);
-            exps(x0, 0);
-            tmem_wait_ld();
-            exps(x2, 1);
             // O to the new maximum before P . V adds to it; a segment's first
             // P . V overwrites O
             if (i > first && __any_sync(0xffffffffu, need)) {
 #pragma unroll 1
-              for (int c0 = 0; c0 < DH; c0 += 32) {
-                tmem_ld32(tO + c0, x0);
+              for (int c0 = 0; c0 < DH; c0 += 8) {
+                uint32_t o[8];
+                tmem_ld8(tO + c0, o);
                 tmem_wait_ld();
 #pragma unroll
-                for (int j = 0; j < 32; ++j)
-                  x0[j] = __float_as_uint(__uint_as_float(x0[j]) * alpha);
-                tmem_st32(tO + c0, x0);
+                for (int j = 0; j < 8; ++j)
+                  o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+                tmem_st8(tO + c0, o);
               }
+            }
+            l *= alpha;
+#pragma unroll
+            for (int g = 0; g < 8; ++g) {
+              const uint64_t c2 = pack2(cg[g], cg[g]), o2 = pack2(lw[g] - m, lw[g] - m);
+              uint64_t sum = 0;
+              uint32_t p[8];
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                float x0, x1;
+                unpack2(fma2(pack2u(s[16 * g + 2 * j], s[16 * g + 2 * j + 1]), c2, o2), x0, x1);
+                const float p0 = ex2(x0), p1 = ex2(x1);
+                sum = add2(sum, pack2(p0, p1));
+                p[j] = pack_f16x2(p0, p1);
+              }
+              float e0, e1;
+              unpack2(sum, e0, e1);
+              l = fmaf(e0 + e1, iw[g], l);
+              tmem_st8(tS + 8 * g, p);
             }
             tmem_wait_st();
           }
@@ -418,39 +464,32 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
     }
   } else if (warp < 12) {
     // ---------------------------------------------- codes to fp16 tiles
-    reg_dec<120>();
+    reg_dec<64>();
     const int tid = threadIdx.x - 256;
     constexpr int NV = kAttnBN * DH / 16 / kConv;  // 16-code chunks per thread
-    constexpr int CPR = DH / 16;                   // chunks per row
-    const int row0 = tid / CPR, col = tid % CPR;   // chunk i: row row0 + i * kConv / CPR
+    // The thread's chunks: column `col` of rows row0, row0 + kConv * 16 / DH,
+    // ...  Eight lanes that access shared memory together read 128 different
+    // bytes of the codes (128-byte rows: columns 0-3 of an even row with 4-7
+    // of the odd one beside it) and, by the swizzle, write eight different
+    // 16-byte bank groups (even ones for an even row, odd ones for an odd).
+    const int half = (tid >> 2) & 1;
+    const int row0 = DH == 64 ? tid >> 2 : ((tid >> 4) << 1) + half;
+    const int col = DH == 64 ? tid & 3 : (tid & 3) + 4 * (half ^ ((tid >> 3) & 1));
     const uint32_t sK = smem_u32(base + SL.k), sV = smem_u32(base + SL.v);
-    uint4 kr[NV], vr[NV];
-    float nk = 1.f, nw = 1.f;  // next tile's scales of group tid (tid < 8)
-    auto load = [&](uint4 (&x)[NV], const uint8_t* p, int nv) {
-#pragma unroll
+    const uint32_t rK = smem_u32(base + SL.raw), rV = rK + kAttnBN * DH;
+    auto convert = [&](uint32_t src, uint32_t dst, int nv) {
+#pragma unroll 4
       for (int i = 0; i < NV; ++i) {
-        const int row = row0 + i * (kConv / CPR);
-        x[i] = row < nv ? ldg_stream(p + (size_t)row * DH + col * 16) : make_uint4(0, 0, 0, 0);
-      }
-    };
-    // Chunk i of the registers as 32 bytes of fp16.  Columns 64.. store their
-    // two 16-byte halves in the other order: eight lanes of a store then hit
-    // eight different bank groups.
-    auto store = [&](const uint4 (&x)[NV], uint32_t dst) {
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int row = row0 + i * (kConv / CPR);
+        const int row = row0 + i * (kConv * 16 / DH);
+        uint4 x = lds128(src + row * DH + col * 16);
+        if (row >= nv) x = make_uint4(0, 0, 0, 0);  // behind the context: zeros
         uint32_t w[8];
-        codes4<TYPE>(x[i].x, w[0], w[1]);
-        codes4<TYPE>(x[i].y, w[2], w[3]);
-        codes4<TYPE>(x[i].z, w[4], w[5]);
-        codes4<TYPE>(x[i].w, w[6], w[7]);
-        const bool odd = col >= 4;
-        const uint32_t a0 = dst + chunk_at(row, 2 * col), a1 = dst + chunk_at(row, 2 * col + 1);
-        sts128(odd ? a1 : a0, odd ? w[4] : w[0], odd ? w[5] : w[1], odd ? w[6] : w[2],
-               odd ? w[7] : w[3]);
-        sts128(odd ? a0 : a1, odd ? w[0] : w[4], odd ? w[1] : w[5], odd ? w[2] : w[6],
-               odd ? w[3] : w[7]);
+        codes4<TYPE>(x.x, w[0], w[1]);
+        codes4<TYPE>(x.y, w[2], w[3]);
+        codes4<TYPE>(x.z, w[4], w[5]);
+        codes4<TYPE>(x.w, w[6], w[7]);
+        sts128(dst + chunk_at(row, 2 * col), w[0], w[1], w[2], w[3]);
+        sts128(dst + chunk_at(row, 2 * col + 1), w[4], w[5], w[6], w[7]);
       }
     };
     // The block's own rows [S, Hkv, dh] (bf16) by a power of two in fp16
@@ -489,56 +528,47 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
       return e;
     };
     int kt = 0, used0 = 0, used1 = 0;  // tiles, uses of each slot
+    int raw = 0;                       // context tiles so far
     bool ok = true;
-    bool have = false;  // the registers hold the tile about to be stored
     while (ok && walk.next(su, sa, sb)) {
       const Unit un = unit_of(a, su);
       const size_t pair = (size_t)un.b * a.Hkv + un.g;
-      const uint8_t* kp = a.k_ctx + pair * a.L_cap * DH;
-      const uint8_t* vp = a.v_ctx + pair * a.L_cap * DH;
       const float* ksp = a.k_scale + pair * a.n_blocks;
       const float* vsp = a.v_scale + pair * a.n_blocks;
+      float nk = 1.f, nw = 1.f;  // a tile's scales of group tid (tid < 8), a tile ahead
       auto load_scales = [&](int tl) {
-        if (tid < 8) {
+        if (tid < 8 && tl > 0 && tl < sb) {
           const int pos = (tl - 1) * kAttnBN + tid * 16;
           nk = pos < un.L ? __ldg(ksp + pos / a.block) : 1.f;
           nw = pos < un.L ? __ldg(vsp + pos / a.block) : 1.f;
         }
       };
-      have = false;
+      load_scales(sa);
       for (int tl = sa; tl < sb; ++tl, ++kt) {
         // the ring: slots by turns, or one slot per chain (each barrier then
         // has one reader that sees its phases in order)
         const int slot = split ? (tl - sa) & 1 : kt & 1;
         const uint32_t par = ((uint32_t)(slot ? used1++ : used0++) & 1u) ^ 1u;
         const uint32_t dK = sK + slot * NSUB * kSub, dV = sV + slot * NSUB * kSub;
-        const bool more = tl + 1 < sb;
-        const size_t key0 = (size_t)(max(tl, 1) - 1) * kAttnBN;
-        if (tl > 0 && !have) {
-          load(kr, kp + key0 * DH, tile_keys(tl, un.L, a.S));
-          load(vr, vp + key0 * DH, tile_keys(tl, un.L, a.S));
-          load_scales(tl);
-        }
-        if (tid == 0 && tl + kL2Ahead < sb) {
-          const size_t at = (size_t)(tl + kL2Ahead - 1) * kAttnBN * DH;
-          const uint32_t n = (uint32_t)tile_keys(tl + kL2Ahead, un.L, a.S) * DH;
-          prefetch_l2_bulk(kp + at, n);
-          prefetch_l2_bulk(vp + at, n);
-        }
-        if (!mbar_wait_inline(&k_empty[slot], par, a.err, abort_flag, WHERE_ATTN_PRODUCER)) {
+        const int nv = tile_keys(tl, un.L, a.S);
+        if ((tl > 0 && !mbar_wait_inline(&rk_full[0], (uint32_t)raw & 1u, a.err, abort_flag,
+                                         WHERE_ATTN_PRODUCER)) ||
+            !mbar_wait_inline(&k_empty[slot], par, a.err, abort_flag, WHERE_ATTN_PRODUCER)) {
           ok = false;
           break;
         }
         int ek = 0, ev = 0;
-        if (tl == 0)
+        if (tl == 0) {
           ek = block_rows(a.k_blk + ((size_t)un.b * a.S * a.Hkv + un.g) * DH, dK, 0);
-        else
-          store(kr, dK);
+        } else {
+          convert(rK, dK, nv);
+          mbar_arrive(&rk_empty[0]);
+        }
         fence_proxy_async_smem();
         mbar_arrive(&k_full[slot]);
-        if (more)
-          load(kr, kp + (size_t)tl * kAttnBN * DH, tile_keys(tl + 1, un.L, a.S));
-        if (!mbar_wait_inline(&v_empty[slot], par, a.err, abort_flag, WHERE_ATTN_PRODUCER)) {
+        if ((tl > 0 && !mbar_wait_inline(&rk_full[1], (uint32_t)raw & 1u, a.err, abort_flag,
+                                         WHERE_ATTN_PRODUCER)) ||
+            !mbar_wait_inline(&v_empty[slot], par, a.err, abort_flag, WHERE_ATTN_PRODUCER)) {
           ok = false;
           break;
         }
@@ -553,21 +583,61 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
           sc[16 + tid] = 1.f / w;
           mbar_arrive(&sc_full[slot]);
         }
-        if (tl > 0) store(vr, dV);
+        load_scales(tl + 1);
+        if (tl > 0) {
+          convert(rV, dV, nv);
+          mbar_arrive(&rk_empty[1]);
+          ++raw;
+        }
         fence_proxy_async_smem();
         mbar_arrive(&v_full[slot]);
-        if (more) {
-          load(vr, vp + (size_t)tl * kAttnBN * DH, tile_keys(tl + 1, un.L, a.S));
-          load_scales(tl + 1);
-        }
-        have = more;
       }
     }
   } else {
-    // ---------------------------------------------------------- MMA issue
-    reg_dec<56>();
+    reg_dec<64>();
     const int ch = warp - 12;
-    if (ch < 2) {
+    if (warp == 14) {
+      // ----------------------------------------- codes to shared memory
+      // One K and one V tile of codes (contiguous in memory) ahead of the
+      // converters, and kL2Ahead tiles brought into L2 before that.
+      if (lane == 0) {
+        const uint32_t rK = smem_u32(base + SL.raw), rV = rK + kAttnBN * DH;
+        int raw = 0;
+        bool ok = true;
+        while (ok && walk.next(su, sa, sb)) {
+          const Unit un = unit_of(a, su);
+          const size_t pair = (size_t)un.b * a.Hkv + un.g;
+          const uint8_t* kp = a.k_ctx + pair * a.L_cap * DH;
+          const uint8_t* vp = a.v_ctx + pair * a.L_cap * DH;
+          auto ahead = [&](int tl) {
+            if (tl > 0 && tl < sb) {
+              const size_t at = (size_t)(tl - 1) * kAttnBN * DH;
+              const uint32_t n = (uint32_t)tile_keys(tl, un.L, a.S) * DH;
+              prefetch_l2_bulk(kp + at, n);
+              prefetch_l2_bulk(vp + at, n);
+            }
+          };
+          for (int k = 1; k < kL2Ahead; ++k) ahead(sa + k);
+          for (int tl = sa; tl < sb; ++tl) {
+            ahead(tl + kL2Ahead);
+            if (tl == 0) continue;
+            const size_t at = (size_t)(tl - 1) * kAttnBN * DH;
+            const uint32_t n = (uint32_t)tile_keys(tl, un.L, a.S) * DH;
+            const uint32_t par = ((uint32_t)raw & 1u) ^ 1u;
+            ok = mbar_wait_inline(&rk_empty[0], par, a.err, abort_flag, WHERE_ATTN_PRODUCER);
+            if (!ok) break;
+            mbar_arrive_expect_tx(&rk_full[0], n);
+            bulk_load(rK, kp + at, n, &rk_full[0]);
+            ok = mbar_wait_inline(&rk_empty[1], par, a.err, abort_flag, WHERE_ATTN_PRODUCER);
+            if (!ok) break;
+            mbar_arrive_expect_tx(&rk_full[1], n);
+            bulk_load(rV, vp + at, n, &rk_full[1]);
+            ++raw;
+          }
+        }
+      }
+    } else if (ch < 2) {
+      // -------------------------------------------------------- MMA issue
       constexpr uint32_t idS = idesc_f16(128, kAttnBN, false), idO = idesc_f16(128, DH, true);
       const uint32_t tS = tmem + ch * kAttnBN, tO = tmem + 2 * kAttnBN + ch * DH;
       const uint64_t dQ = sdesc_sw128(smem_u32(base + SL.q) + ch * NSUB * kSub, 16, 1024);
@@ -616,7 +686,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
 #pragma unroll
             for (int k = 0; k < kAttnBN / 16; ++k)
               if (k < ksteps)
-                umma_bf16_ts(tO, tS + kPCol + k * 8, dV + (uint64_t)(k * (2048 >> 4)), idO,
+                umma_bf16_ts(tO, tS + k * 8, dV + (uint64_t)(k * (2048 >> 4)), idO,
                              (i > first || k > 0) ? 1u : 0u);
             umma_commit(&v_empty[slot]);
             if (i + step >= sb) umma_commit(&o_full[ch]);
