@@ -273,7 +273,11 @@ static AttnGeom attn_geom(const tt_dims& d) {
 
 AttnShape attn_shape(const tt_dims& d) {
   const AttnGeom g = attn_geom(d);
-  return AttnShape{g.G, g.s_per_half, g.rows_per_half, g.halves, g.n_qtiles, g.units, g.n_ctas};
+  // no more CTAs than there can be tiles
+  const long long t_max = (long long)g.units * (1 + (d.L_cap + kAttnBN - 1) / kAttnBN);
+  return AttnShape{g.G,        g.s_per_half, g.rows_per_half,
+                   g.halves,   g.n_qtiles,   g.units,
+                   (int)std::min<long long>(g.n_ctas, t_max)};
 }
 
 // K splits of the linear-update GEMM: enough (tile, K range) units to fill

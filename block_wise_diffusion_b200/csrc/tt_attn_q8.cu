@@ -55,7 +55,7 @@ __host__ __device__ constexpr Smem smem_layout(int dh) {
   s.raw = s.v + kSlots * nsub * kSub;    // codes of one K and one V tile
   s.scales = s.raw + 2 * kAttnBN * dh;  // [slot][key scale, log2 w, 1 / w][8 groups]
   s.bars = (s.scales + kSlots * 24 * 4 + 63) / 64 * 64;
-  s.total = s.bars + 256;
+  s.total = s.bars + 320;
   return s;
 }
 
@@ -248,7 +248,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
   uint64_t* sc_full = v_empty + kSlots;  // [slot]
   uint64_t* rk_full = sc_full + kSlots;  // [K, V] a tile of codes has landed
   uint64_t* rk_empty = rk_full + 2;      // [K, V] it has been converted
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(rk_empty + 2);
+  uint64_t* turn = rk_empty + 2;         // [chain][row quarter] exponentials done
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(turn + 8);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
   uint32_t* red = tmem_slot + 2;  // [8] converter reduction
 
@@ -272,6 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
       mbar_init(&v_empty[s], users);
       mbar_init(&sc_full[s], 8);
     }
+    for (int i = 0; i < 8; ++i) mbar_init(&turn[i], 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -408,6 +410,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
               }
             }
             l *= alpha;
+            // Chains that see the same tiles take turns at the exponentials, so
+            // that the tensor core works for one while MUFU works for the other
+            // (side by side they would both wait for the one, then the other).
+            if (!split && (ch == 1 || pt > 0) &&
+                !mbar_wait_inline(&turn[4 * (ch ^ 1) + (warp & 3)],
+                                  (uint32_t)(ch == 1 ? pt : pt - 1) & 1u, a.err, abort_flag,
+                                  WHERE_ATTN_SOFTMAX)) {
+              ok = false;
+              break;
+            }
 #pragma unroll
             for (int g = 0; g < 8; ++g) {
               const uint64_t c2 = pack2(cg[g], cg[g]), o2 = pack2(lw[g] - m, lw[g] - m);
@@ -425,6 +437,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
               unpack2(sum, e0, e1);
               l = fmaf(e0 + e1, iw[g], l);
               tmem_st8(tS + 8 * g, p);
+            }
+            if (!split) {
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&turn[4 * ch + (warp & 3)]);
             }
             tmem_wait_st();
           }
@@ -478,10 +494,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
     const uint32_t sK = smem_u32(base + SL.k), sV = smem_u32(base + SL.v);
     const uint32_t rK = smem_u32(base + SL.raw), rV = rK + kAttnBN * DH;
     auto convert = [&](uint32_t src, uint32_t dst, int nv) {
-#pragma unroll 4
+      uint4 v[NV];
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        v[i] = lds128(src + (row0 + i * (kConv * 16 / DH)) * DH + col * 16);
+#pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int row = row0 + i * (kConv * 16 / DH);
-        uint4 x = lds128(src + row * DH + col * 16);
+        uint4 x = v[i];
         if (row >= nv) x = make_uint4(0, 0, 0, 0);  // behind the context: zeros
         uint32_t w[8];
         codes4<TYPE>(x.x, w[0], w[1]);
