@@ -14,8 +14,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libtwotower.so")
 SOURCES = ["tt_api.cu", "tt_gemm.cu", "tt_attn.cu", "tt_small.cu", "tt_noalloc.cu",
-           "tt_api_q8.cu", "tt_attn_q8.cu", "tt_cache_q8.cu", "tt_gemm_i8.cu"]
-HEADERS = ["tt_internal.h", "tt_ptx.cuh", "tt_q8.h", "tt_quant.cuh",
+           "tt_api_q8.cu", "tt_attn_q8.cu", "tt_attn_q8_rows.cu", "tt_cache_q8.cu", "tt_gemm_i8.cu"]
+HEADERS = ["tt_internal.h", "tt_ptx.cuh", "tt_q8.h", "tt_quant.cuh", "tt_attn_q8.cuh",
            os.path.join("..", "..", "include", "twotower.h")]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = [

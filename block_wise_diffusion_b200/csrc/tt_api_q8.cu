@@ -72,22 +72,19 @@ struct Carver {
 
 // -------------------------------------------------------------- attention
 struct AttnQ8Ws {
-  int *ctrl, *tile_start, *first_unit, *unit_done;
-  int4* unit_ctas;
+  int *ctrl, *seq_start;
   float *part_o, *part_ml;
   size_t total;
 };
 AttnQ8Ws carve_attn(const tt_dims& d, const AttnShape& g, void* ws) {
   Carver c{reinterpret_cast<uint8_t*>(ws)};
   AttnQ8Ws w;
+  const size_t rows = d.S * g.G <= kRowsMax ? kRowsMax : 256;
   const size_t slots = (size_t)g.units + g.n_ctas - 1;
   w.ctrl = c.take<int>(kCtrlBytes);
-  w.tile_start = c.take<int>((size_t)(g.units + 1) * sizeof(int));
-  w.first_unit = c.take<int>((size_t)g.n_ctas * sizeof(int));
-  w.unit_ctas = c.take<int4>((size_t)g.units * sizeof(int4));
-  w.unit_done = c.take<int>((size_t)g.units * sizeof(int));
-  w.part_o = c.take<float>(slots * 256 * d.dh * sizeof(float));
-  w.part_ml = c.take<float>(slots * 256 * 2 * sizeof(float));
+  w.seq_start = c.take<int>((size_t)(d.B + 1) * sizeof(int));
+  w.part_o = c.take<float>(slots * rows * d.dh * sizeof(float));
+  w.part_ml = c.take<float>(slots * rows * 2 * sizeof(float));
   w.total = c.total();
   return w;
 }
@@ -194,6 +191,9 @@ tt_status tt_block_denoise_attn_q8(const tt_dims* d, const tt_q8* f, const tt_bf
   Q8_CHECK(check_ptr(ctx_len, "ctx_len", 4));
   Q8_CHECK(check_ptr(out, "out", 16));
   const AttnShape g = attn_shape(*d);
+  if ((long long)d->B * d->Hkv * g.n_qtiles * (1ll + (d->L_cap + kAttnBN - 1) / kAttnBN) >=
+      (1ll << 31) - 2048)
+    return set_errorf(TT_ERR_UNSUPPORTED, "problem too large");
   const AttnQ8Ws w = carve_attn(*d, g, ws);
   Q8_CHECK(check_ws_ptr(ws, ws_bytes, w.total));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
@@ -223,28 +223,17 @@ tt_status tt_block_denoise_attn_q8(const tt_dims* d, const tt_q8* f, const tt_bf
   a.n_qtiles = g.n_qtiles;
   a.units = g.units;
   a.n_ctas = g.n_ctas;
-  a.tile_start = w.tile_start;
-  a.first_unit = w.first_unit;
-  a.unit_ctas = w.unit_ctas;
+  a.seq_start = w.seq_start;
   a.part_o = w.part_o;
   a.part_ml = w.part_ml;
   a.err = w.ctrl;
-  AttnArgs plan{};
-  plan.Hkv = d->Hkv;
-  plan.L_cap = d->L_cap;
-  plan.ctx_len = ctx_len;
-  plan.n_qtiles = g.n_qtiles;
-  plan.units = g.units;
-  plan.n_ctas = g.n_ctas;
-  plan.tile_start = w.tile_start;
-  plan.first_unit = w.first_unit;
-  plan.unit_ctas = w.unit_ctas;
-  plan.unit_done = w.unit_done;
-  plan.err = w.ctrl;
-  Q8_CUDA(cudaMemsetAsync(w.ctrl, 0, kCtrlBytes, st));
-  Q8_LAUNCH(TT_K_ATTN_PLAN, st, launch_attn_plan(plan, st));
-  Q8_LAUNCH(TT_K_ATTN_Q8, st, launch_attn_q8(a, f->type, st));
-  Q8_LAUNCH(TT_K_MERGE_Q8, st, launch_attn_q8_merge(a, st));
+  if (d->S * g.G <= kRowsMax) {
+    Q8_LAUNCH(TT_K_ATTN_Q8, st, launch_attn_q8_rows(a, f->type, st));
+    Q8_LAUNCH(TT_K_MERGE_Q8, st, launch_attn_q8_rows_merge(a, st));
+  } else {
+    Q8_LAUNCH(TT_K_ATTN_Q8, st, launch_attn_q8(a, f->type, st));
+    Q8_LAUNCH(TT_K_MERGE_Q8, st, launch_attn_q8_merge(a, st));
+  }
   return TT_OK;
 }
 

@@ -14,8 +14,7 @@
 // values are brought into fp16 range by a power of two per row (per tile),
 // which is exact down to 2^-28 of the largest magnitude.
 //
-// Units, tiles and the balanced persistent schedule are those of the bf16
-// kernel (attn_plan_kernel).  Inside a CTA two chains run side by side, each
+// Inside a CTA (tt_attn_q8.cuh has the schedule) two chains run side by side, each
 // with 128 query rows, 128 TMEM columns of S / P and dh of O:
 //   S = Q . K(tile)^T -> softmax -> O += P . V(tile) -> next S ...
 // With more than 128 rows per KV head the chains take the two halves of the
@@ -29,8 +28,7 @@
 //   warp 14           codes from global to shared memory.
 #include <math.h>
 
-#include "tt_q8.h"
-#include "tt_ptx.cuh"
+#include "tt_attn_q8.cuh"
 
 namespace tt {
 
@@ -66,77 +64,6 @@ __device__ __forceinline__ uint8_t* align1024(uint8_t* p) {
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn_major) {
   return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) |
          ((uint32_t)(M >> 4) << 24);
-}
-
-// The CTA's range of the tile sequence, one unit's part at a time.
-struct Walk {
-  const int* start;
-  int t, hi, u;
-  __device__ __forceinline__ bool next(int& unit, int& a, int& b) {
-    if (t >= hi) return false;
-    const int s0 = start[u], s1 = start[u + 1];
-    unit = u++;
-    a = t - s0;
-    t = min(hi, s1);
-    b = t - s0;
-    return true;
-  }
-};
-
-struct Unit {
-  int b, g, qt, L;
-};
-__device__ __forceinline__ Unit unit_of(const AttnQ8Args& a, int u) {
-  Unit x;
-  const int pair = u / a.n_qtiles;
-  x.qt = u - pair * a.n_qtiles;
-  x.b = pair / a.Hkv;
-  x.g = pair - x.b * a.Hkv;
-  x.L = min(max(a.ctx_len[x.b], 0), a.L_cap);
-  return x;
-}
-// Valid keys of local tile t (0: the block's own keys).
-__device__ __forceinline__ int tile_keys(int t, int L, int S) {
-  return t == 0 ? S : min(kAttnBN, L - (t - 1) * kAttnBN);
-}
-
-// 2^e, e in [-126, 127]
-__device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
-
-// Exponent e with amax 2^-e in [2^14, 2^15), for the bf16 magnitude bits amax
-// (clamped so that 2^e and 2^-e are normal; 0 for zero and for non-finite).
-__device__ __forceinline__ int norm_exp(uint32_t amax) {
-  const int e = (int)(amax >> 7);
-  return e == 0 || e == 255 ? 0 : min(max(e - 127 - 14, -126), 126);
-}
-
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-// bf16 pair times a power of two, as an fp16 pair
-__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t w, float f) {
-  return pack_f16x2(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xFFFF0000u) * f);
-}
-
-// Four codes to two fp16 pairs.  int8: the byte with its sign bit flipped is
-// the code + 128, which as the low byte of 0x64xx makes 1024 + 128 + code.
-template <int TYPE>
-__device__ __forceinline__ void codes4(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  if constexpr (TYPE == TT_Q8_INT8) {
-    const uint32_t u = w ^ 0x80808080u;
-    asm("prmt.b32 %0, %2, %3, 0x4140;\n\tprmt.b32 %1, %2, %3, 0x4342;"
-        : "=r"(lo), "=r"(hi)
-        : "r"(u), "r"(0x64646464u));
-    asm("sub.f16x2 %0, %0, %1;" : "+r"(lo) : "r"(0x64806480u));
-    asm("sub.f16x2 %0, %0, %1;" : "+r"(hi) : "r"(0x64806480u));
-  } else {
-    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-        : "=r"(lo), "=r"(hi)
-        : "r"(w));
-  }
 }
 
 // Pairs of fp32 in one 64-bit register: one instruction for two.
@@ -218,18 +145,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
   griddep_launch();
   griddep_wait();
   extern __shared__ uint8_t smem_raw[];
-  const int cta = blockIdx.x;
-  const long long T = a.tile_start[a.units];
-  const int lo = (int)((long long)cta * T / a.n_ctas);
-  const int hi = (int)((long long)(cta + 1) * T / a.n_ctas);
-  const int u0 = a.first_unit[cta];
-  if (lo >= hi) {
-    // An empty range lies inside the CTA range of at most one unit, the one
-    // that holds tile lo and starts before it: an empty record for the merge.
-    if (a.tile_start[u0] < lo)
+  __shared__ PlanSmem plan;
+  TileWalk walk = plan_walk<kThreads>(a, plan);
+  const int U = a.Hkv * a.n_qtiles;
+  if (walk.left == 0) {
+    if (walk.off > 0) {  // an empty range inside a unit: an empty record
+      const size_t slot = (size_t)walk.b * U + walk.k + blockIdx.x;
       for (int i = threadIdx.x; i < 256; i += kThreads)
-        *reinterpret_cast<float2*>(a.part_ml + ((size_t)(u0 + cta) * 256 + i) * 2) =
-            make_float2(-INFINITY, 0.f);
+        reinterpret_cast<float2*>(a.part_ml)[slot * 256 + i] = make_float2(-INFINITY, 0.f);
+    }
     return;
   }
   constexpr int NSUB = DH / 64;
@@ -285,8 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  Walk walk{a.tile_start, lo, hi, u0};
-  int su, sa, sb;  // current segment: unit, local tiles [sa, sb)
+  int ub, uk, sa, sb, L;  // current segment: sequence, unit in it, local tiles [sa, sb), length
 
   if (warp < 8) {
     // ------------------------------------------------------------ softmax
@@ -301,14 +224,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
     const bool busy = (warp & 3) * 32 < a.rows_per_half;  // the warp has a row
     int kt = 0, pt = 0, qi = 0;                           // tiles of the CTA, turns, segments
     bool ok = true;
-    for (; ok && walk.next(su, sa, sb); kt += sb - sa) {
-      const Unit un = unit_of(a, su);
-      const int slot = su + cta;
+    for (; ok && walk.next(ub, uk, sa, sb, L); kt += sb - sa) {
+      const int ug = uk / a.n_qtiles, qt = uk - ug * a.n_qtiles;
+      const size_t slot = (size_t)ub * U + uk + blockIdx.x;
       const int step = split ? 2 : 1, first = sa + (split ? ch : 0);
       float m = -INFINITY, l = 0.f;
-      const int s_pos = un.qt * a.halves * a.s_per_half + (split ? 0 : ch * a.s_per_half) + r / a.G;
-      const int head = un.g * a.G + r % a.G;
-      const size_t qrow = (size_t)(un.b * a.S + s_pos) * a.Hq + head;
+      const int s_pos = qt * a.halves * a.s_per_half + (split ? 0 : ch * a.s_per_half) + r / a.G;
+      const size_t qrow = ((size_t)ub * a.S + s_pos) * a.Hq + ug * a.G + r % a.G;
       if (first < sb) {
         // The query row, by a power of two in fp16 range.  The previous
         // segment's last S of this chain has been waited for below.
@@ -368,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
             tmem_ld32(tS + 64, *reinterpret_cast<uint32_t(*)[32]>(&s[64]));
             tmem_ld32(tS + 96, *reinterpret_cast<uint32_t(*)[32]>(&s[96]));
             tmem_wait_ld();
-            const int nv = tile_keys(i, un.L, a.S);
+            const int nv = tile_keys(i, L, a.S);
             if (nv < kAttnBN) {
 #pragma unroll
               for (int j = 0; j < 128; ++j)
@@ -455,17 +377,29 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
         ++qi;
         tc_fence_after();
       }
-      // The segment's partial: unnormalised O (tile-major [slot][dh/4][256
+      // A unit that this CTA holds alone, in rows of its own, is done; other
+      // segments leave a partial: unnormalised O (tile-major [dh/4][256
       // rows][4], a warp's store is 512 contiguous bytes) and (m, l).
       const int r256 = ch * 128 + r;
+      const bool whole = !split && sa == 0 && sb == 1 + (L + kAttnBN - 1) / kAttnBN;
       if (busy && first < sb) {
-        float* po = a.part_o + (size_t)slot * DH * 256 + (size_t)r256 * 4;
+        float* po = a.part_o + slot * DH * 256 + (size_t)r256 * 4;
+        const float inv = 1.f / l;
 #pragma unroll 1
         for (int c0 = 0; c0 < DH; c0 += 32) {
           uint32_t o[32];
           tmem_ld32(tO + c0, o);
           tmem_wait_ld();
-          if (valid) {
+          if (valid && whole) {
+            uint32_t w[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              w[j] = pack_bf16x2(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+              *reinterpret_cast<uint4*>(a.out + qrow * DH + c0 + 8 * v) =
+                  make_uint4(w[4 * v], w[4 * v + 1], w[4 * v + 2], w[4 * v + 3]);
+          } else if (valid) {
 #pragma unroll
             for (int v = 0; v < 8; ++v)
               *reinterpret_cast<float4*>(po + (size_t)(c0 / 4 + v) * 1024) =
@@ -474,9 +408,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
           }
         }
       }
-      if (valid)
-        *reinterpret_cast<float2*>(a.part_ml + ((size_t)slot * 256 + r256) * 2) =
-            make_float2(m, l);
+      if (valid && !whole)
+        reinterpret_cast<float2*>(a.part_ml)[slot * 256 + r256] = make_float2(m, l);
     }
   } else if (warp < 12) {
     // ---------------------------------------------- codes to fp16 tiles
@@ -550,17 +483,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
     int kt = 0, used0 = 0, used1 = 0;  // tiles, uses of each slot
     int raw = 0;                       // context tiles so far
     bool ok = true;
-    while (ok && walk.next(su, sa, sb)) {
-      const Unit un = unit_of(a, su);
-      const size_t pair = (size_t)un.b * a.Hkv + un.g;
+    while (ok && walk.next(ub, uk, sa, sb, L)) {
+      const int ug = uk / a.n_qtiles;
+      const size_t pair = (size_t)ub * a.Hkv + ug;
       const float* ksp = a.k_scale + pair * a.n_blocks;
       const float* vsp = a.v_scale + pair * a.n_blocks;
       float nk = 1.f, nw = 1.f;  // a tile's scales of group tid (tid < 8), a tile ahead
       auto load_scales = [&](int tl) {
         if (tid < 8 && tl > 0 && tl < sb) {
           const int pos = (tl - 1) * kAttnBN + tid * 16;
-          nk = pos < un.L ? __ldg(ksp + pos / a.block) : 1.f;
-          nw = pos < un.L ? __ldg(vsp + pos / a.block) : 1.f;
+          nk = pos < L ? __ldg(ksp + pos / a.block) : 1.f;
+          nw = pos < L ? __ldg(vsp + pos / a.block) : 1.f;
         }
       };
       load_scales(sa);
@@ -570,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
         const int slot = split ? (tl - sa) & 1 : kt & 1;
         const uint32_t par = ((uint32_t)(slot ? used1++ : used0++) & 1u) ^ 1u;
         const uint32_t dK = sK + slot * NSUB * kSub, dV = sV + slot * NSUB * kSub;
-        const int nv = tile_keys(tl, un.L, a.S);
+        const int nv = tile_keys(tl, L, a.S);
         if ((tl > 0 && !mbar_wait_inline(&rk_full[0], (uint32_t)raw & 1u, a.err, abort_flag,
                                          WHERE_ATTN_PRODUCER)) ||
             !mbar_wait_inline(&k_empty[slot], par, a.err, abort_flag, WHERE_ATTN_PRODUCER)) {
@@ -579,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
         }
         int ek = 0, ev = 0;
         if (tl == 0) {
-          ek = block_rows(a.k_blk + ((size_t)un.b * a.S * a.Hkv + un.g) * DH, dK, 0);
+          ek = block_rows(a.k_blk + ((size_t)ub * a.S * a.Hkv + ug) * DH, dK, 0);
         } else {
           convert(rK, dK, nv);
           mbar_arrive(&rk_empty[0]);
@@ -594,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
         }
         // The scales go with V: once P . V of the tile that had the slot
         // before has run, the softmax is done with that tile's scales.
-        if (tl == 0) ev = block_rows(a.v_blk + ((size_t)un.b * a.S * a.Hkv + un.g) * DH, dV, 1);
+        if (tl == 0) ev = block_rows(a.v_blk + ((size_t)ub * a.S * a.Hkv + ug) * DH, dV, 1);
         if (tid < 8) {
           float* sc = scales + slot * 24;
           const float w = tl == 0 ? pow2i(ev) : nw;
@@ -624,15 +557,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
         const uint32_t rK = smem_u32(base + SL.raw), rV = rK + kAttnBN * DH;
         int raw = 0;
         bool ok = true;
-        while (ok && walk.next(su, sa, sb)) {
-          const Unit un = unit_of(a, su);
-          const size_t pair = (size_t)un.b * a.Hkv + un.g;
+        while (ok && walk.next(ub, uk, sa, sb, L)) {
+          const size_t pair = (size_t)ub * a.Hkv + uk / a.n_qtiles;
           const uint8_t* kp = a.k_ctx + pair * a.L_cap * DH;
           const uint8_t* vp = a.v_ctx + pair * a.L_cap * DH;
           auto ahead = [&](int tl) {
             if (tl > 0 && tl < sb) {
               const size_t at = (size_t)(tl - 1) * kAttnBN * DH;
-              const uint32_t n = (uint32_t)tile_keys(tl, un.L, a.S) * DH;
+              const uint32_t n = (uint32_t)tile_keys(tl, L, a.S) * DH;
               prefetch_l2_bulk(kp + at, n);
               prefetch_l2_bulk(vp + at, n);
             }
@@ -642,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
             ahead(tl + kL2Ahead);
             if (tl == 0) continue;
             const size_t at = (size_t)(tl - 1) * kAttnBN * DH;
-            const uint32_t n = (uint32_t)tile_keys(tl, un.L, a.S) * DH;
+            const uint32_t n = (uint32_t)tile_keys(tl, L, a.S) * DH;
             const uint32_t par = ((uint32_t)raw & 1u) ^ 1u;
             ok = mbar_wait_inline(&rk_empty[0], par, a.err, abort_flag, WHERE_ATTN_PRODUCER);
             if (!ok) break;
@@ -665,8 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
       const uint64_t dV0 = sdesc_sw128(smem_u32(base + SL.v), kSub, 1024);
       int kt = 0, pt = 0, qi = 0;
       bool ok = true;
-      for (; ok && walk.next(su, sa, sb); kt += sb - sa) {
-        const int L = unit_of(a, su).L;
+      for (; ok && walk.next(ub, uk, sa, sb, L); kt += sb - sa) {
         const int step = split ? 2 : 1, first = sa + (split ? ch : 0);
         if (first >= sb) continue;
         auto scores = [&](int i, int turn) -> bool {
@@ -741,8 +672,9 @@ __global__ void __launch_bounds__(256) attn_q8_merge_kernel(const AttnQ8Args a) 
   if (u >= a.units) return;
   const int h = row >> 7, r = row & 127;
   if (r >= a.rows_per_half) return;
-  const int4 uc = a.unit_ctas[u];
+  const int2 uc = unit_ctas(a, u);
   const int per = a.halves == 1 ? 2 : 1;  // partials per segment
+  if (per == 1 && uc.x == uc.y) return;   // written by its CTA
   const int n = (uc.y - uc.x + 1) * per;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float den = 0.f, mrun = -INFINITY;

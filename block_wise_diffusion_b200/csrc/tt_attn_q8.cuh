@@ -1,0 +1,188 @@
+// What the 8-bit attention kernels share: the schedule, code conversion and
+// the exact handling of ranges.
+//
+// Schedule.  A unit is (sequence, KV head, query tile); all units of a
+// sequence have the same number of key tiles (tile 0: the block's own keys,
+// then 128 context keys each), so the tile sequence is described by prefix
+// sums over the B sequences alone, and every CTA computes them itself from
+// ctx_len instead of waiting for a planning kernel.  CTA c takes the tiles
+// [c T / P, (c + 1) T / P) of the T tiles; its part of unit u (a segment) has
+// the partial record u + c, which no other segment has.
+#pragma once
+#include "tt_q8.h"
+#include "tt_ptx.cuh"
+
+namespace tt {
+
+// One position in the tile sequence and what is left of the CTA's range.
+struct TileWalk {
+  const int* ctx_len;
+  long long left;  // tiles of the range not yet handed out
+  int L_cap, U;    // units per sequence
+  int b, k;        // sequence, unit within it
+  int off;         // tile within the unit
+  // The next segment: unit (b, k), local tiles [a, e), context length L.
+  __device__ __forceinline__ bool next(int& sb, int& sk, int& a, int& e, int& L) {
+    if (left <= 0) return false;
+    L = min(max(ctx_len[b], 0), L_cap);
+    const int n = 1 + (L + kAttnBN - 1) / kAttnBN;
+    sb = b;
+    sk = k;
+    a = off;
+    e = (int)min((long long)n, off + left);
+    left -= e - a;
+    off = 0;
+    if (++k == U) {
+      k = 0;
+      ++b;
+    }
+    return true;
+  }
+};
+
+struct PlanSmem {
+  long long warp_tot[32];
+  long long total, pre;
+  int b, bad;
+};
+
+// Every thread of the CTA: the CTA's walk.  CTA 0 also stores the prefix sums
+// over sequences for the merge, and starts the error word (an out-of-range
+// length is clamped and recorded).  NT: threads of the CTA.
+template <int NT>
+__device__ __forceinline__ TileWalk plan_walk(const AttnQ8Args& a, PlanSmem& sm) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (a.B + NT - 1) / NT;
+  const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
+  auto tiles = [&](int b, int& bad) {
+    const int L = a.ctx_len[b];
+    bad |= L < 0 || L > a.L_cap;
+    return 1 + (min(max(L, 0), a.L_cap) + kAttnBN - 1) / kAttnBN;
+  };
+  long long sum = 0;
+  int bad = 0;
+  for (int b = b0; b < b1; ++b) sum += tiles(b, bad);
+  long long incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) sm.warp_tot[warp] = incl;
+  bad = __syncthreads_or(bad);
+  long long before = 0, total = 0;
+  for (int w = 0; w < NT / 32; ++w) {
+    const long long x = sm.warp_tot[w];
+    before += w < warp ? x : 0;
+    total += x;
+  }
+  const int U = a.Hkv * a.n_qtiles;
+  const long long T = total * U;
+  const long long lo = (long long)blockIdx.x * T / a.n_ctas;
+  const long long hi = (long long)(blockIdx.x + 1) * T / a.n_ctas;
+  long long pre = before + incl - sum;
+  if (blockIdx.x == 0) {
+    long long p = pre;
+    int x = 0;
+    for (int b = b0; b < b1; ++b) {
+      a.seq_start[b] = (int)p;
+      p += tiles(b, x);
+    }
+    if (tid == 0) {
+      a.seq_start[a.B] = (int)total;
+      a.err[0] = bad ? (int)TT_ERR_INVALID_ARG : 0;
+      a.err[1] = 0;
+    }
+  }
+  if (lo >= pre * U && lo < (pre + sum) * U) {  // exactly one thread
+    int b = b0, x = 0;
+    for (;; ++b) {
+      const int n = tiles(b, x);
+      if (lo < (pre + n) * U) break;
+      pre += n;
+    }
+    sm.b = b;
+    sm.pre = pre;
+  }
+  __syncthreads();
+  TileWalk w;
+  w.ctx_len = a.ctx_len;
+  w.L_cap = a.L_cap;
+  w.U = U;
+  w.left = hi - lo;
+  w.b = sm.b;
+  int x = 0;
+  const int n = tiles(w.b, x);
+  const int rem = (int)(lo - sm.pre * U);
+  w.k = rem / n;
+  w.off = rem - w.k * n;
+  return w;
+}
+
+// Valid keys of local tile t (0: the block's own keys).
+__device__ __forceinline__ int tile_keys(int t, int L, int S) {
+  return t == 0 ? S : min(kAttnBN, L - (t - 1) * kAttnBN);
+}
+
+// The CTAs that hold a unit's tiles (all of [x, y] have a record, an empty
+// range inside the unit an empty one).
+__device__ __forceinline__ int2 unit_ctas(const AttnQ8Args& a, long long u) {
+  const int U = a.Hkv * a.n_qtiles;
+  const int b = (int)(u / U), k = (int)(u - (long long)b * U);
+  const int p0 = a.seq_start[b], n = a.seq_start[b + 1] - p0;
+  const long long T = (long long)a.seq_start[a.B] * U;
+  const long long s0 = (long long)p0 * U + (long long)k * n, s1 = s0 + n;
+  return make_int2((int)(((s0 + 1) * a.n_ctas - 1) / T), (int)((s1 * a.n_ctas - 1) / T));
+}
+
+// 2^e, e in [-126, 127]
+__device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
+
+// Exponent e with amax 2^-e in [2^14, 2^15), for the bf16 magnitude bits amax
+// (clamped so that 2^e and 2^-e are normal; 0 for zero and for non-finite).
+__device__ __forceinline__ int norm_exp(uint32_t amax) {
+  const int e = (int)(amax >> 7);
+  return e == 0 || e == 255 ? 0 : min(max(e - 127 - 14, -126), 126);
+}
+// Two running maxima (packed) of bf16 magnitudes.
+__device__ __forceinline__ uint32_t absmax_bf16x8(uint32_t m, const uint4& v) {
+  m = __vmaxu2(m, v.x & 0x7FFF7FFFu);
+  m = __vmaxu2(m, v.y & 0x7FFF7FFFu);
+  m = __vmaxu2(m, v.z & 0x7FFF7FFFu);
+  return __vmaxu2(m, v.w & 0x7FFF7FFFu);
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// bf16 pair times a power of two, as an fp16 pair
+__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t w, float f) {
+  return pack_f16x2(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xFFFF0000u) * f);
+}
+
+// Two codes in the low 16 bits (after int8 codes had their sign bits flipped)
+// to an fp16 pair.  int8: the flipped byte is the code + 128, which as the
+// low byte of 0x64xx makes 1024 + 128 + code.
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("sub.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
+// Four codes to two fp16 pairs.
+template <int TYPE>
+__device__ __forceinline__ void codes4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if constexpr (TYPE == TT_Q8_INT8) {
+    const uint32_t u = w ^ 0x80808080u;
+    lo = sub_f16x2(__byte_perm(u, 0x64646464u, 0x4140), 0x64806480u);
+    hi = sub_f16x2(__byte_perm(u, 0x64646464u, 0x4342), 0x64806480u);
+  } else {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+  }
+}
+
+}  // namespace tt

@@ -1,0 +1,423 @@
+// Block-denoise attention over an 8-bit cache for at most 16 query rows per
+// KV head (the autoregressive step: one position and up to 16 heads).
+//
+// With so few rows the work is streaming the cache: 2 dh bytes per key
+// against 16 rows of arithmetic, far below the tensor cores' rate, so what
+// matters is bytes in flight and instructions per byte.  The codes go from
+// global memory straight into the operand registers of warp-level matrix
+// instructions (m16n8k16, fp16): no shared memory and no barrier on the way.
+// That works because the order of dh inside a product is free:
+//   S = Q K^T   lane (n, c) = (lane / 4, lane % 4) loads dh/4 consecutive codes
+//               of key n; its word j is exactly the operand of step j;
+//   O += P V    lane (n, c) loads dh/8 consecutive codes (columns n dh/8 ..) of
+//               the keys 2c, 2c+1, 2c+8, 2c+9; byte j of a pair of keys is the
+//               operand of column tile j.
+// Each warp takes every 8th group of 32 keys with a running maximum and sum
+// of its own (the formulas of tt_attn_q8.cu) and refills a register buffer as
+// soon as the products have read it.  The 8 warps' results are joined through
+// shared memory at a segment's end.
+#include <math.h>
+
+#include "tt_attn_q8.cuh"
+
+namespace tt {
+
+namespace {
+
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kGroup = 32;          // keys per step of a warp
+constexpr float kRescale = 8.0f;    // log2 units the running maximum may lag
+
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// N codes-words from global memory, not kept in L1.
+template <int N>
+__device__ __forceinline__ void load_words(uint32_t (&x)[N], const uint8_t* p) {
+  if constexpr (N == 2) {
+    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];"
+                 : "=r"(x[0]), "=r"(x[1])
+                 : "l"(p));
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 4)
+      asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(x[i]), "=r"(x[i + 1]), "=r"(x[i + 2]), "=r"(x[i + 3])
+                   : "l"(p + 4 * i));
+  }
+}
+
+template <int TYPE, int DH>
+__global__ void __launch_bounds__(kThreads, 1) attn_q8_rows_kernel(const AttnQ8Args a) {
+  griddep_launch();
+  griddep_wait();
+  extern __shared__ __align__(16) float sm_o[];  // [warp][16][DH + 4]
+  __shared__ PlanSmem plan;
+  __shared__ float sm_m[kWarps][16], sm_l[kWarps][16];
+  constexpr int KW = DH / 16;  // words of a key per lane (K side), steps of Q K^T
+  constexpr int VW = DH / 32;  // words of a key per lane (V side)
+  constexpr int NT = DH / 8;   // column tiles of O
+  constexpr int LDO = DH + 4;
+  TileWalk walk = plan_walk<kThreads>(a, plan);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int n8 = lane >> 2, c4 = lane & 3;
+  const int rows = a.rows_per_half;
+  if (walk.left == 0) {
+    if (walk.off > 0) {  // an empty range inside a unit: an empty record
+      const size_t slot = (size_t)walk.b * a.Hkv + walk.k + blockIdx.x;
+      if (threadIdx.x < 16)
+        reinterpret_cast<float2*>(a.part_ml)[slot * 16 + threadIdx.x] = make_float2(-INFINITY, 0.f);
+    }
+    return;
+  }
+  int ub, ug, sa, sb, L;
+  while (walk.next(ub, ug, sa, sb, L)) {
+    const size_t pair = (size_t)ub * a.Hkv + ug;
+    // ---- Q: rows n8 and n8 + 8, each brought into fp16 range by a power of two
+    uint32_t q[KW][4];
+    float c_row[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int r = n8 + 8 * h;
+      uint4 x[DH / 32];
+      uint32_t mx = 0;
+      // row r = position r / G of the block, head r % G
+      const uint16_t* p = a.q + (((size_t)ub * a.S + r / a.G) * a.Hq + ug * a.G + r % a.G) * DH +
+                          c4 * (DH / 4);
+#pragma unroll
+      for (int i = 0; i < DH / 32; ++i) {
+        x[i] = r < rows ? reinterpret_cast<const uint4*>(p)[i] : make_uint4(0, 0, 0, 0);
+        mx = absmax_bf16x8(mx, x[i]);
+      }
+      mx = max(mx & 0xFFFFu, mx >> 16);
+      mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      const int e = norm_exp(mx);
+      const float f = pow2i(-e);
+      c_row[h] = a.scale_log2 * pow2i(e);
+#pragma unroll
+      for (int i = 0; i < DH / 32; ++i) {
+        q[2 * i][h] = bf16x2_to_f16x2(x[i].x, f);
+        q[2 * i][2 + h] = bf16x2_to_f16x2(x[i].y, f);
+        q[2 * i + 1][h] = bf16x2_to_f16x2(x[i].z, f);
+        q[2 * i + 1][2 + h] = bf16x2_to_f16x2(x[i].w, f);
+      }
+    }
+    float o[NT][4];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+
+    // Softmax of NTILE 8-key tiles of scores (16 keys share a scale) and its
+    // product with V: `vfrag(t16, j, b0, b1)` gives the operand of keys
+    // t16*16.. and column tile j.  nv: valid keys.
+    auto finish = [&](auto& s, const float* sk, const float* lw, const float* iw, int nv,
+                      auto&& vfrag) {
+      constexpr int N16 = sizeof(s) / sizeof(s[0]) / 2;
+#pragma unroll
+      for (int t = 0; t < 2 * N16; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (t * 8 + c4 * 2 + e >= nv) s[t][e] = s[t][2 + e] = -INFINITY;
+      float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int g = 0; g < N16; ++g)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float y = fmaxf(fmaxf(s[2 * g][2 * h], s[2 * g][2 * h + 1]),
+                                fmaxf(s[2 * g + 1][2 * h], s[2 * g + 1][2 * h + 1]));
+          mx[h] = fmaxf(mx[h], fmaf(y, c_row[h] * sk[g], lw[g]));
+        }
+      bool need = false;
+      float alpha[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
+        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
+        alpha[h] = 1.f;
+        if (mx[h] > m[h] + kRescale) {
+          alpha[h] = ex2(m[h] - mx[h]);
+          m[h] = mx[h];
+          need = true;
+        }
+      }
+      if (__any_sync(0xffffffffu, need)) {
+        l[0] *= alpha[0];
+        l[1] *= alpha[1];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          o[j][0] *= alpha[0];
+          o[j][1] *= alpha[0];
+          o[j][2] *= alpha[1];
+          o[j][3] *= alpha[1];
+        }
+      }
+#pragma unroll
+      for (int g = 0; g < N16; ++g) {
+        uint32_t p[4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float cg = c_row[h] * sk[g], off = lw[g] - m[h];
+          const float p0 = ex2(fmaf(s[2 * g][2 * h], cg, off));
+          const float p1 = ex2(fmaf(s[2 * g][2 * h + 1], cg, off));
+          const float p2 = ex2(fmaf(s[2 * g + 1][2 * h], cg, off));
+          const float p3 = ex2(fmaf(s[2 * g + 1][2 * h + 1], cg, off));
+          l[h] = fmaf((p0 + p1) + (p2 + p3), iw[g], l[h]);
+          p[h] = pack_f16x2(p0, p1);
+          p[2 + h] = pack_f16x2(p2, p3);
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          uint32_t b0, b1;
+          vfrag(g, j, b0, b1);
+          mma16816(o[j], p, b0, b1);
+        }
+      }
+    };
+
+    // ---- the context keys of the segment, group by group
+    const int key_lo = (max(sa, 1) - 1) * kAttnBN, key_hi = min((sb - 1) * kAttnBN, L);
+    const uint8_t* kp = a.k_ctx + pair * a.L_cap * DH + (size_t)n8 * DH + c4 * (DH / 4);
+    const uint8_t* vp = a.v_ctx + pair * a.L_cap * DH + (size_t)(2 * c4) * DH + n8 * (DH / 8);
+    const float* ksp = a.k_scale + pair * a.n_blocks;
+    const float* vsp = a.v_scale + pair * a.n_blocks;
+    uint32_t kr[4][KW], vr[8][VW];
+    auto load_k = [&](int key0) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        if (key0 + t * 8 + n8 < key_hi) {
+          load_words(kr[t], kp + (size_t)(key0 + t * 8) * DH);
+        } else {
+#pragma unroll
+          for (int i = 0; i < KW; ++i) kr[t][i] = 0;
+        }
+      }
+    };
+    // vr[4 g + i]: key 16 g + 2 c4 + {0, 1, 8, 9}[i]
+    auto load_v = [&](int key0) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int at = (i >> 2) * 16 + (i & 1) + ((i >> 1) & 1) * 8;
+        if (key0 + at + 2 * c4 < key_hi) {
+          load_words(vr[i], vp + (size_t)(key0 + at) * DH);
+        } else {
+#pragma unroll
+          for (int w = 0; w < VW; ++w) vr[i][w] = 0;
+        }
+      }
+    };
+    float nks[2], nvs[2];
+    auto load_scales = [&](int key0) {
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const int pos = key0 + 16 * g;
+        nks[g] = pos < key_hi ? __ldg(ksp + pos / a.block) : 1.f;
+        nvs[g] = pos < key_hi ? __ldg(vsp + pos / a.block) : 1.f;
+      }
+    };
+    int key0 = key_lo + warp * kGroup;
+    if (key0 < key_hi) {
+      load_k(key0);
+      load_v(key0);
+      load_scales(key0);
+    }
+    // ---- the block's own keys (at most 16), by one warp while the others start
+    if (sa == 0 && warp == kWarps - 1) {
+      const int S = a.S;
+      uint32_t bk[2][2 * KW], bv[4][2 * VW];  // bf16
+      uint32_t mk = 0, mv = 0;
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const int key = t * 8 + n8;
+        const uint16_t* p = a.k_blk + (((size_t)ub * S + key) * a.Hkv + ug) * DH + c4 * (DH / 4);
+#pragma unroll
+        for (int i = 0; i < KW / 2; ++i) {
+          const uint4 x = key < S ? reinterpret_cast<const uint4*>(p)[i] : make_uint4(0, 0, 0, 0);
+          mk = absmax_bf16x8(mk, x);
+          bk[t][4 * i] = x.x, bk[t][4 * i + 1] = x.y, bk[t][4 * i + 2] = x.z, bk[t][4 * i + 3] = x.w;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int key = 2 * c4 + (i & 1) + (i >> 1) * 8;
+        const uint16_t* p = a.v_blk + (((size_t)ub * S + key) * a.Hkv + ug) * DH + n8 * (DH / 8);
+#pragma unroll
+        for (int w = 0; w < VW / 2; ++w) {
+          const uint4 x = key < S ? reinterpret_cast<const uint4*>(p)[w] : make_uint4(0, 0, 0, 0);
+          mv = absmax_bf16x8(mv, x);
+          bv[i][4 * w] = x.x, bv[i][4 * w + 1] = x.y, bv[i][4 * w + 2] = x.z, bv[i][4 * w + 3] = x.w;
+        }
+      }
+      const int ek = norm_exp(__reduce_max_sync(0xffffffffu, max(mk & 0xFFFFu, mk >> 16)));
+      const int ev = norm_exp(__reduce_max_sync(0xffffffffu, max(mv & 0xFFFFu, mv >> 16)));
+      const float fk = pow2i(-ek), fv = pow2i(-ev);
+      float s[2][4];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
+#pragma unroll
+        for (int j = 0; j < KW; ++j)
+          mma16816(s[t], q[j], bf16x2_to_f16x2(bk[t][2 * j], fk),
+                   bf16x2_to_f16x2(bk[t][2 * j + 1], fk));
+      }
+      const float sk[1] = {pow2i(ek)}, lw[1] = {(float)ev}, iw[1] = {pow2i(-ev)};
+      finish(s, sk, lw, iw, S, [&](int, int j, uint32_t& b0, uint32_t& b1) {
+        // value j of each key: half a word
+        auto v = [&](int i) {
+          const uint32_t w = bv[i][j >> 1];
+          return __uint_as_float(j & 1 ? w & 0xFFFF0000u : w << 16) * fv;
+        };
+        b0 = pack_f16x2(v(0), v(1));
+        b1 = pack_f16x2(v(2), v(3));
+      });
+    }
+    for (; key0 < key_hi; key0 += kWarps * kGroup) {
+      const int next = key0 + kWarps * kGroup;
+      float sk[2], lw[2], iw[2];
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        sk[g] = nks[g];
+        lw[g] = log2f(nvs[g]);
+        iw[g] = 1.f / nvs[g];
+      }
+      float s[4][4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
+#pragma unroll
+      for (int j = 0; j < KW; ++j)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          uint32_t b0, b1;
+          codes4<TYPE>(kr[t][j], b0, b1);
+          mma16816(s[t], q[j], b0, b1);
+        }
+      if (next < key_hi) {
+        load_k(next);
+        load_scales(next);
+      }
+      finish(s, sk, lw, iw, key_hi - key0, [&](int g, int j, uint32_t& b0, uint32_t& b1) {
+        // byte j of a pair of keys, for two pairs: (k0, k1, k8, k9) as one word
+        const uint32_t x = __byte_perm(vr[4 * g][j >> 2], vr[4 * g + 1][j >> 2],
+                                       (j & 3) | ((4 + (j & 3)) << 4));
+        const uint32_t y = __byte_perm(vr[4 * g + 2][j >> 2], vr[4 * g + 3][j >> 2],
+                                       (j & 3) | ((4 + (j & 3)) << 4));
+        codes4<TYPE>(__byte_perm(x, y, 0x5410), b0, b1);
+      });
+      if (next < key_hi) load_v(next);
+    }
+
+    // ---- the warps' results: o[j] holds columns (2 c4 + {0, 1}) DH/8 + j of
+    // rows n8 (first two) and n8 + 8
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+      if (c4 == 0) {
+        sm_m[warp][n8 + 8 * h] = m[h];
+        sm_l[warp][n8 + 8 * h] = l[h];
+      }
+      float* dst = sm_o + (size_t)(warp * 16 + n8 + 8 * h) * LDO + 2 * c4 * (DH / 8);
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int j = 0; j < NT; j += 4)
+          *reinterpret_cast<float4*>(dst + e * (DH / 8) + j) =
+              make_float4(o[j][2 * h + e], o[j + 1][2 * h + e], o[j + 2][2 * h + e],
+                          o[j + 3][2 * h + e]);
+    }
+    __syncthreads();
+    const size_t slot = pair + blockIdx.x;
+    const bool whole = sa == 0 && sb == 1 + (L + kAttnBN - 1) / kAttnBN;
+    for (int i = threadIdx.x; i < rows * (DH / 4); i += kThreads) {
+      const int r = i / (DH / 4), col = (i - r * (DH / 4)) * 4;
+      float mr = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) mr = sm_l[w][r] == 0.f ? mr : fmaxf(mr, sm_m[w][r]);
+      float den = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        if (sm_l[w][r] == 0.f) continue;  // this warp had no keys
+        const float f = ex2(sm_m[w][r] - mr);
+        const float4 x = *reinterpret_cast<const float4*>(sm_o + (size_t)(w * 16 + r) * LDO + col);
+        den = fmaf(f, sm_l[w][r], den);
+        acc.x = fmaf(f, x.x, acc.x);
+        acc.y = fmaf(f, x.y, acc.y);
+        acc.z = fmaf(f, x.z, acc.z);
+        acc.w = fmaf(f, x.w, acc.w);
+      }
+      if (whole) {
+        const float inv = 1.f / den;
+        uint16_t* dst = a.out + (((size_t)ub * a.S + r / a.G) * a.Hq + ug * a.G + r % a.G) * DH + col;
+        *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv),
+                                                    pack_bf16x2(acc.z * inv, acc.w * inv));
+      } else {
+        reinterpret_cast<float4*>(a.part_o)[(slot * 16 + r) * (DH / 4) + col / 4] = acc;
+        if (col == 0) reinterpret_cast<float2*>(a.part_ml)[slot * 16 + r] = make_float2(mr, den);
+      }
+    }
+    __syncthreads();  // before the next segment's results
+  }
+}
+
+// CTA = unit: joins the partial records of a unit that several CTAs hold.
+__global__ void __launch_bounds__(128) attn_q8_rows_merge_kernel(const AttnQ8Args a) {
+  griddep_launch();
+  griddep_wait();
+  const long long u = blockIdx.x;
+  const int2 uc = unit_ctas(a, u);
+  if (uc.x == uc.y) return;  // written by its CTA
+  const int b = (int)(u / a.Hkv), g = (int)(u - (long long)b * a.Hkv), dv = a.dh / 4;
+  for (int i = threadIdx.x; i < a.rows_per_half * dv; i += 128) {
+    const int r = i / dv, v = i - r * dv;
+    float mr = -INFINITY, den = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = uc.x; c <= uc.y; ++c) {
+      const size_t slot = (size_t)u + c;
+      const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + slot * 16 + r);
+      if (ml.y == 0.f) continue;
+      const float4 x = __ldcg(reinterpret_cast<const float4*>(a.part_o) + (slot * 16 + r) * dv + v);
+      const float mn = ml.x > mr ? ml.x : mr;
+      const float f0 = ex2(mr - mn), f1 = ex2(ml.x - mn);
+      mr = mn;
+      den = fmaf(den, f0, ml.y * f1);
+      acc.x = fmaf(acc.x, f0, x.x * f1);
+      acc.y = fmaf(acc.y, f0, x.y * f1);
+      acc.z = fmaf(acc.z, f0, x.z * f1);
+      acc.w = fmaf(acc.w, f0, x.w * f1);
+    }
+    const float inv = 1.f / den;
+    uint16_t* dst =
+        a.out + (((size_t)b * a.S + r / a.G) * a.Hq + g * a.G + r % a.G) * a.dh + v * 4;
+    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv),
+                                                pack_bf16x2(acc.z * inv, acc.w * inv));
+  }
+}
+
+template <int TYPE, int DH>
+cudaError_t launch_rows(const AttnQ8Args& a, cudaStream_t st) {
+  constexpr size_t smem = (size_t)kWarps * 16 * (DH + 4) * sizeof(float);
+  cudaError_t e = cudaFuncSetAttribute(attn_q8_rows_kernel<TYPE, DH>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  return launch_k(attn_q8_rows_kernel<TYPE, DH>, dim3(a.n_ctas), dim3(kThreads), smem, st, a);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_q8_rows(const AttnQ8Args& a, int type, cudaStream_t st) {
+  if (type == TT_Q8_INT8)
+    return a.dh == 64 ? launch_rows<TT_Q8_INT8, 64>(a, st) : launch_rows<TT_Q8_INT8, 128>(a, st);
+  return a.dh == 64 ? launch_rows<TT_Q8_E4M3, 64>(a, st) : launch_rows<TT_Q8_E4M3, 128>(a, st);
+}
+cudaError_t launch_attn_q8_rows_merge(const AttnQ8Args& a, cudaStream_t st) {
+  return launch_k(attn_q8_rows_merge_kernel, dim3((unsigned)a.units), dim3(128), 0, st, a);
+}
+
+}  // namespace tt

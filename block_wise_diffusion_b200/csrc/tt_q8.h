@@ -45,7 +45,8 @@ cudaError_t launch_gemm_i8_linear(const CUtensorMap& tmA, const CUtensorMap& tmB
                                   const GemmI8Args& a, int grid, cudaStream_t st);
 
 // --------------------------------------------------------------- attention
-// Units, tiles and CTA ranges as AttnArgs describes them.
+// Units, query tiles and the partition of key tiles are those of the bf16
+// call; see tt_attn_q8.cuh for the schedule.
 struct AttnQ8Args {
   int B, S, Hq, Hkv, dh, G, L_cap, block, n_blocks;
   const uint16_t *q, *k_blk, *v_blk;
@@ -55,15 +56,18 @@ struct AttnQ8Args {
   float scale_log2;  // log2(e) / sqrt(dh)
   uint16_t* out;
   int s_per_half, rows_per_half, halves, n_qtiles, units, n_ctas;
-  const int* tile_start;   // the plan: [units + 1], [n_ctas], [units]
-  const int* first_unit;
-  const int4* unit_ctas;
-  float* part_o;   // [units + n_ctas - 1][dh/4][256][4] unnormalised outputs
-  float* part_ml;  // [units + n_ctas - 1][256][2]: maximum (log2 units), sum
+  int* seq_start;  // [B + 1] key tiles per unit of the sequences before (written by CTA 0)
+  float* part_o;   // [units + n_ctas - 1] unnormalised outputs of segments:
+                   // [dh/4][256 rows][4], or [16 rows][dh] (at most 16 rows)
+  float* part_ml;  // [units + n_ctas - 1][256 or 16 rows][2]: maximum (log2 units), sum
   int* err;
 };
 cudaError_t launch_attn_q8(const AttnQ8Args& a, int type, cudaStream_t st);
 cudaError_t launch_attn_q8_merge(const AttnQ8Args& a, cudaStream_t st);
+// At most kRowsMax query rows per KV head.
+constexpr int kRowsMax = 16;
+cudaError_t launch_attn_q8_rows(const AttnQ8Args& a, int type, cudaStream_t st);
+cudaError_t launch_attn_q8_rows_merge(const AttnQ8Args& a, cudaStream_t st);
 
 // Query packing and CTA count of an attention call, as the bf16 call has them.
 struct AttnShape {
