@@ -205,7 +205,7 @@ tt_status tt_block_denoise_attn_q8(const tt_dims* d, const tt_q8* f, const tt_bf
   a.dh = d->dh;
   a.G = d->Hq / d->Hkv;
   a.L_cap = d->L_cap;
-  a.block = f->block;
+  a.block_shift = f->block == 16 ? 4 : f->block == 32 ? 5 : f->block == 64 ? 6 : 7;
   a.n_blocks = (d->L_cap + f->block - 1) / f->block;
   a.q = q_blk;
   a.k_blk = k_blk;

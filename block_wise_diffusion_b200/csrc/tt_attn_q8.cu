@@ -14,18 +14,24 @@
 // values are brought into fp16 range by a power of two per row (per tile),
 // which is exact down to 2^-28 of the largest magnitude.
 //
-// Inside a CTA (tt_attn_q8.cuh has the schedule) two chains run side by side, each
-// with 128 query rows, 128 TMEM columns of S / P and dh of O:
+// Inside a CTA (tt_attn_q8.cuh has the schedule) two chains run side by side,
+// each with 128 query rows and dh TMEM columns of O:
 //   S = Q . K(tile)^T -> softmax -> O += P . V(tile) -> next S ...
 // With more than 128 rows per KV head the chains take the two halves of the
 // rows and every tile; otherwise they share the rows and take every other
-// tile, so the tensor core works for one while the softmax runs for the other.
+// tile.  The softmax (thread = row) moves the 128 scores of its row to
+// registers at once, so ONE S buffer serves both chains by turns, the other
+// 128 columns hold a P of its own for each chain, and the next S does not
+// wait for this tile's softmax and P . V: with S and P in the same columns
+// (two S buffers) every tile paid S, softmax and P . V one after the other,
+// 4,900 cycles for the two chains where this order takes @@.
 // Roles (16 warps; registers are moved to the softmax by setmaxnreg):
-//   warps 0-3 / 4-7   softmax of chain 0 / 1, thread = row;
+//   warps 0-3 / 4-7   softmax of chain 0 / 1;
 //   warps 8-11        codes of one tile in shared memory to fp16 in the swizzled
 //                     K and V rings;
-//   warps 12, 13      MMA issue of chain 0 / 1 (12 owns TMEM);
-//   warp 14           codes from global to shared memory.
+//   warps 12, 13      issue of S and of P . V for both chains (12 owns TMEM);
+//   warp 14           codes from global to shared memory;
+//   warp 15           the tiles' scales.
 #include <math.h>
 
 #include "tt_attn_q8.cuh"
@@ -53,7 +59,7 @@ __host__ __device__ constexpr Smem smem_layout(int dh) {
   s.raw = s.v + kSlots * nsub * kSub;    // codes of one K and one V tile
   s.scales = s.raw + 2 * kAttnBN * dh;  // [slot][key scale, log2 w, 1 / w][8 groups]
   s.bars = (s.scales + kSlots * 24 * 4 + 63) / 64 * 64;
-  s.total = s.bars + 320;
+  s.total = s.bars + 256;
   return s;
 }
 
@@ -112,6 +118,18 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       "l"(src), "r"(bytes), "r"(smem_u32(bar))
       : "memory");
 }
+// One lane of a converged warp.  Under this predicate, unlike under lane == 0,
+// the operands of an MMA stay in uniform registers: issuing one costs 80
+// cycles instead of 120, and 16 of them stand between P and the next scores.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   uint4 v;
   asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
@@ -140,6 +158,41 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, ui
                : "memory");
 }
 
+// Scales of 16 keys (group g) of a tile: key scale, log2 and inverse of the
+// value scale.
+__device__ __forceinline__ void put_scales(float* sc, int g, float kf, float lw, float iw,
+                                           uint64_t* full) {
+  sc[g] = kf;
+  sc[8 + g] = lw;
+  sc[16 + g] = iw;
+  mbar_arrive(full);
+}
+__device__ __forceinline__ void lds4f(uint32_t addr, float (&v)[4]) {
+  asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+               : "r"(addr));
+}
+
+// 16 of a row's scores to probabilities, as fp16 pairs, and their part of the
+// row sum.  kf: key scale, lw: log2 of the value scale, iw: its inverse.
+__device__ __forceinline__ void exps16(const uint32_t* s, float kf, float lw, float iw, float c_row,
+                                       float m, float& l, uint32_t (&p)[8]) {
+  const float c = c_row * kf, off = lw - m;
+  const uint64_t c2 = pack2(c, c), o2 = pack2(off, off);
+  uint64_t sum = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    float x0, x1;
+    unpack2(fma2(pack2u(s[2 * j], s[2 * j + 1]), c2, o2), x0, x1);
+    const float p0 = ex2(x0), p1 = ex2(x1);
+    sum = add2(sum, pack2(p0, p1));
+    p[j] = pack_f16x2(p0, p1);
+  }
+  float e0, e1;
+  unpack2(sum, e0, e1);
+  l = fmaf(e0 + e1, iw, l);
+}
+
 template <int TYPE, int DH>
 __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a) {
   griddep_launch();
@@ -161,48 +214,47 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
   uint8_t* base = align1024(smem_raw);
   float* scales = reinterpret_cast<float*>(base + SL.scales);
   uint64_t* bars = reinterpret_cast<uint64_t*>(base + SL.bars);
-  uint64_t* q_full = bars;              // [chain] query rows written
-  uint64_t* s_full = q_full + 2;        // [chain] S ready, the P . V before it done
-  uint64_t* p_full = s_full + 2;        // [chain] P written, O corrected
-  uint64_t* o_full = p_full + 2;        // [chain] the segment's last P . V done
-  uint64_t* k_full = o_full + 2;        // [slot]
-  uint64_t* k_empty = k_full + kSlots;  // [slot]
+  uint64_t* q_full = bars;               // [chain] query rows written
+  uint64_t* s_full = q_full + 2;         // [chain] S holds the chain's scores
+  uint64_t* s_free = s_full + 2;         // S is in registers
+  uint64_t* p_full = s_free + 1;         // [chain] P written, O corrected
+  uint64_t* pv_done = p_full + 2;        // [chain] P . V done
+  uint64_t* k_full = pv_done + 2;        // [slot]
+  uint64_t* k_empty = k_full + kSlots;   // [slot]
   uint64_t* v_full = k_empty + kSlots;
   uint64_t* v_empty = v_full + kSlots;
   uint64_t* sc_full = v_empty + kSlots;  // [slot]
   uint64_t* rk_full = sc_full + kSlots;  // [K, V] a tile of codes has landed
   uint64_t* rk_empty = rk_full + 2;      // [K, V] it has been converted
-  uint64_t* turn = rk_empty + 2;         // [chain][row quarter] exponentials done
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(turn + 8);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(rk_empty + 2);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
   uint32_t* red = tmem_slot + 2;  // [8] converter reduction
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (the shuffle tells the compiler that the index is the same in all lanes)
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const bool split = a.halves == 1;  // the chains share the rows and split the tiles
-  constexpr uint32_t kTmemCols = 2 * (kAttnBN + DH) <= 256 ? 256 : 512;
   if (threadIdx.x == 0) {
-    const int users = split ? 1 : 2;  // chains that read a K / V slot
+    mbar_init(s_free, 128);
     for (int c = 0; c < 2; ++c) {
       mbar_init(&q_full[c], 128);
       mbar_init(&s_full[c], 1);
       mbar_init(&p_full[c], 128);
-      mbar_init(&o_full[c], 1);
+      mbar_init(&pv_done[c], 1);
       mbar_init(&rk_full[c], 1);
       mbar_init(&rk_empty[c], kConv);
     }
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(&k_full[s], kConv);
-      mbar_init(&k_empty[s], users);
+      mbar_init(&k_empty[s], 1);
       mbar_init(&v_full[s], kConv);
-      mbar_init(&v_empty[s], users);
+      mbar_init(&v_empty[s], 1);
       mbar_init(&sc_full[s], 8);
     }
-    for (int i = 0; i < 8; ++i) mbar_init(&turn[i], 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
   if (warp == 12) {
-    tmem_alloc(tmem_slot, kTmemCols);
+    tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -217,14 +269,32 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
     const int ch = warp >> 2;
     const int r = threadIdx.x & 127;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t tS = tmem + ch * kAttnBN + lane_off;
+    const uint32_t tS = tmem + lane_off, tP = tmem + kAttnBN + ch * 64 + lane_off;
     const uint32_t tO = tmem + 2 * kAttnBN + ch * DH + lane_off;
     const uint32_t sQ = smem_u32(base + SL.q) + ch * NSUB * kSub;
     const bool valid = r < a.rows_per_half;
     const bool busy = (warp & 3) * 32 < a.rows_per_half;  // the warp has a row
-    int kt = 0, pt = 0, qi = 0;                           // tiles of the CTA, turns, segments
+    int kt = 0, pt = 0;                                   // tiles of the CTA, turns
     bool ok = true;
-    for (; ok && walk.next(ub, uk, sa, sb, L); kt += sb - sa) {
+    if (!busy) {
+      // no rows in this warp: its part of the barriers alone
+      while (ok && walk.next(ub, uk, sa, sb, L)) {
+        const int step = split ? 2 : 1, first = sa + (split ? ch : 0);
+        if (first >= sb) continue;
+        mbar_arrive(&q_full[ch]);
+        for (int i = first; i < sb; i += step, ++pt) {
+          ok = mbar_wait_inline(&s_full[ch], (uint32_t)pt & 1u, a.err, abort_flag,
+                                WHERE_ATTN_SOFTMAX);
+          if (!ok) break;
+          mbar_arrive(s_free);
+          mbar_arrive(&p_full[ch]);
+          ok = mbar_wait_inline(&pv_done[ch], (uint32_t)pt & 1u, a.err, abort_flag,
+                                WHERE_ATTN_SOFTMAX);
+          if (!ok) break;
+        }
+      }
+    }
+    for (; busy && ok && walk.next(ub, uk, sa, sb, L); kt += sb - sa) {
       const int ug = uk / a.n_qtiles, qt = uk - ug * a.n_qtiles;
       const size_t slot = (size_t)ub * U + uk + blockIdx.x;
       const int step = split ? 2 : 1, first = sa + (split ? ch : 0);
@@ -267,39 +337,40 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
             ok = false;
             break;
           }
-          float cg[8], lw[8], iw[8];  // per 16 keys: score factor, log2 w, 1 / w
-#pragma unroll
-          for (int g = 0; g < 8; g += 4) {
-            const float4* sc = reinterpret_cast<const float4*>(scales + ts * 24 + g);
-            const float4 x = sc[0], y = sc[2], z = sc[4];
-            cg[g] = c_row * x.x, cg[g + 1] = c_row * x.y;
-            cg[g + 2] = c_row * x.z, cg[g + 3] = c_row * x.w;
-            lw[g] = y.x, lw[g + 1] = y.y, lw[g + 2] = y.z, lw[g + 3] = y.w;
-            iw[g] = z.x, iw[g + 1] = z.y, iw[g + 2] = z.z, iw[g + 3] = z.w;
-          }
+          const uint32_t sc = smem_u32(scales + ts * 24);
           if (!mbar_wait_inline(&s_full[ch], (uint32_t)pt & 1u, a.err, abort_flag,
                                 WHERE_ATTN_SOFTMAX)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          if (busy) {
-            uint32_t s[128];
-            tmem_ld32(tS, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
-            tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
-            tmem_ld32(tS + 64, *reinterpret_cast<uint32_t(*)[32]>(&s[64]));
-            tmem_ld32(tS + 96, *reinterpret_cast<uint32_t(*)[32]>(&s[96]));
-            tmem_wait_ld();
-            const int nv = tile_keys(i, L, a.S);
-            if (nv < kAttnBN) {
+          uint32_t s[128];
+          tmem_ld32(tS, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
+          tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
+          tmem_ld32(tS + 64, *reinterpret_cast<uint32_t(*)[32]>(&s[64]));
+          tmem_ld32(tS + 96, *reinterpret_cast<uint32_t(*)[32]>(&s[96]));
+          tmem_wait_ld();
+          tc_fence_before();
+          mbar_arrive(s_free);
+          float alpha = 1.f;
+          bool need = false;
+          uint32_t p0[8], p1[8];
+          float kf[4], lw[4], iw[4];
+          const int nv = tile_keys(i, L, a.S);
+          if (nv < kAttnBN) {
 #pragma unroll
-              for (int j = 0; j < 128; ++j)
-                if (j >= nv) s[j] = __float_as_uint(-INFINITY);
-            }
-            float gm[8];
+            for (int j = 0; j < 128; ++j)
+              if (j >= nv) s[j] = __float_as_uint(-INFINITY);
+          }
+          float mx = -INFINITY;
 #pragma unroll
-            for (int g = 0; g < 8; ++g) {
-              const uint32_t* x = s + 16 * g;
+          for (int g = 0; g < 8; g += 4) {
+            float kf[4], lw[4];
+            lds4f(sc + 4 * g, kf);
+            lds4f(sc + 32 + 4 * g, lw);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t* x = s + 16 * (g + k);
               float y0 = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
               float y1 = fmaxf(__uint_as_float(x[2]), __uint_as_float(x[3]));
 #pragma unroll
@@ -307,74 +378,68 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
                 y0 = fmax3(y0, __uint_as_float(x[j]), __uint_as_float(x[j + 1]));
                 y1 = fmax3(y1, __uint_as_float(x[j + 2]), __uint_as_float(x[j + 3]));
               }
-              gm[g] = fmaf(fmaxf(y0, y1), cg[g], lw[g]);
+              mx = fmaxf(mx, fmaf(fmaxf(y0, y1), c_row * kf[k], lw[k]));
             }
-            const float mx = fmaxf(fmax3(fmax3(gm[0], gm[1], gm[2]), gm[3], gm[4]),
-                                   fmax3(gm[5], gm[6], gm[7]));
-            const bool need = mx > m + kRescale;
-            float alpha = 1.f;
-            if (need) {
-              alpha = ex2(m - mx);
-              m = mx;
-            }
-            // O to the new maximum before P . V adds to it; a segment's first
-            // P . V overwrites O
-            if (i > first && __any_sync(0xffffffffu, need)) {
-#pragma unroll 1
-              for (int c0 = 0; c0 < DH; c0 += 8) {
-                uint32_t o[8];
-                tmem_ld8(tO + c0, o);
-                tmem_wait_ld();
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                  o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
-                tmem_st8(tO + c0, o);
-              }
-            }
-            l *= alpha;
-            // Chains that see the same tiles take turns at the exponentials, so
-            // that the tensor core works for one while MUFU works for the other
-            // (side by side they would both wait for the one, then the other).
-            if (!split && (ch == 1 || pt > 0) &&
-                !mbar_wait_inline(&turn[4 * (ch ^ 1) + (warp & 3)],
-                                  (uint32_t)(ch == 1 ? pt : pt - 1) & 1u, a.err, abort_flag,
-                                  WHERE_ATTN_SOFTMAX)) {
-              ok = false;
-              break;
-            }
-#pragma unroll
-            for (int g = 0; g < 8; ++g) {
-              const uint64_t c2 = pack2(cg[g], cg[g]), o2 = pack2(lw[g] - m, lw[g] - m);
-              uint64_t sum = 0;
-              uint32_t p[8];
-#pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                float x0, x1;
-                unpack2(fma2(pack2u(s[16 * g + 2 * j], s[16 * g + 2 * j + 1]), c2, o2), x0, x1);
-                const float p0 = ex2(x0), p1 = ex2(x1);
-                sum = add2(sum, pack2(p0, p1));
-                p[j] = pack_f16x2(p0, p1);
-              }
-              float e0, e1;
-              unpack2(sum, e0, e1);
-              l = fmaf(e0 + e1, iw[g], l);
-              tmem_st8(tS + 8 * g, p);
-            }
-            if (!split) {
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&turn[4 * ch + (warp & 3)]);
-            }
-            tmem_wait_st();
           }
+          need = mx > m + kRescale;
+          if (need) {
+            alpha = ex2(m - mx);
+            m = mx;
+          }
+          l *= alpha;
+          lds4f(sc, kf);
+          lds4f(sc + 32, lw);
+          lds4f(sc + 64, iw);
+          exps16(s, kf[0], lw[0], iw[0], c_row, m, l, p0);
+          exps16(s + 16, kf[1], lw[1], iw[1], c_row, m, l, p1);
+          // P and O are the tensor core's until P . V of the turn before has run
+          if (i > first && !mbar_wait_inline(&pv_done[ch], (uint32_t)(pt - 1) & 1u, a.err,
+                                             abort_flag, WHERE_ATTN_SOFTMAX)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          // O to the new maximum before P . V adds to it; a segment's first
+          // P . V overwrites O
+          if (i > first && __any_sync(0xffffffffu, need)) {
+#pragma unroll 1
+            for (int c0 = 0; c0 < DH; c0 += 8) {
+              uint32_t o[8];
+              tmem_ld8(tO + c0, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+              tmem_st8(tO + c0, o);
+            }
+          }
+          tmem_st8(tP, p0);
+          tmem_st8(tP + 8, p1);
+          exps16(s + 32, kf[2], lw[2], iw[2], c_row, m, l, p0);
+          tmem_st8(tP + 16, p0);
+          exps16(s + 48, kf[3], lw[3], iw[3], c_row, m, l, p1);
+          tmem_st8(tP + 24, p1);
+          lds4f(sc + 16, kf);
+          lds4f(sc + 48, lw);
+          lds4f(sc + 80, iw);
+          exps16(s + 64, kf[0], lw[0], iw[0], c_row, m, l, p0);
+          tmem_st8(tP + 32, p0);
+          exps16(s + 80, kf[1], lw[1], iw[1], c_row, m, l, p1);
+          tmem_st8(tP + 40, p1);
+          exps16(s + 96, kf[2], lw[2], iw[2], c_row, m, l, p0);
+          tmem_st8(tP + 48, p0);
+          exps16(s + 112, kf[3], lw[3], iw[3], c_row, m, l, p1);
+          tmem_st8(tP + 56, p1);
+          tmem_wait_st();
           tc_fence_before();
           mbar_arrive(&p_full[ch]);
         }
         if (!ok) break;
-        if (!mbar_wait_inline(&o_full[ch], (uint32_t)qi & 1u, a.err, abort_flag, WHERE_ATTN_SOFTMAX)) {
+        if (!mbar_wait_inline(&pv_done[ch], (uint32_t)(pt - 1) & 1u, a.err, abort_flag,
+                              WHERE_ATTN_SOFTMAX)) {
           ok = false;
           break;
         }
-        ++qi;
         tc_fence_after();
       }
       // A unit that this CTA holds alone, in rows of its own, is done; other
@@ -382,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
       // rows][4], a warp's store is 512 contiguous bytes) and (m, l).
       const int r256 = ch * 128 + r;
       const bool whole = !split && sa == 0 && sb == 1 + (L + kAttnBN - 1) / kAttnBN;
-      if (busy && first < sb) {
+      if (first < sb) {
         float* po = a.part_o + slot * DH * 256 + (size_t)r256 * 4;
         const float inv = 1.f / l;
 #pragma unroll 1
@@ -485,18 +550,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
     bool ok = true;
     while (ok && walk.next(ub, uk, sa, sb, L)) {
       const int ug = uk / a.n_qtiles;
-      const size_t pair = (size_t)ub * a.Hkv + ug;
-      const float* ksp = a.k_scale + pair * a.n_blocks;
-      const float* vsp = a.v_scale + pair * a.n_blocks;
-      float nk = 1.f, nw = 1.f;  // a tile's scales of group tid (tid < 8), a tile ahead
-      auto load_scales = [&](int tl) {
-        if (tid < 8 && tl > 0 && tl < sb) {
-          const int pos = (tl - 1) * kAttnBN + tid * 16;
-          nk = pos < L ? __ldg(ksp + pos / a.block) : 1.f;
-          nw = pos < L ? __ldg(vsp + pos / a.block) : 1.f;
-        }
-      };
-      load_scales(sa);
       for (int tl = sa; tl < sb; ++tl, ++kt) {
         // the ring: slots by turns, or one slot per chain (each barrier then
         // has one reader that sees its phases in order)
@@ -525,18 +578,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
           ok = false;
           break;
         }
-        // The scales go with V: once P . V of the tile that had the slot
-        // before has run, the softmax is done with that tile's scales.
-        if (tl == 0) ev = block_rows(a.v_blk + ((size_t)ub * a.S * a.Hkv + ug) * DH, dV, 1);
-        if (tid < 8) {
-          float* sc = scales + slot * 24;
-          const float w = tl == 0 ? pow2i(ev) : nw;
-          sc[tid] = tl == 0 ? pow2i(ek) : nk;
-          sc[8 + tid] = tl == 0 ? (float)ev : log2f(w);
-          sc[16 + tid] = 1.f / w;
-          mbar_arrive(&sc_full[slot]);
+        if (tl == 0) {
+          ev = block_rows(a.v_blk + ((size_t)ub * a.S * a.Hkv + ug) * DH, dV, 1);
+          if (tid < 8) put_scales(scales + slot * 24, tid, pow2i(ek), (float)ev, pow2i(-ev), &sc_full[slot]);
         }
-        load_scales(tl + 1);
         if (tl > 0) {
           convert(rV, dV, nv);
           mbar_arrive(&rk_empty[1]);
@@ -548,7 +593,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
     }
   } else {
     reg_dec<64>();
-    const int ch = warp - 12;
     if (warp == 14) {
       // ----------------------------------------- codes to shared memory
       // One K and one V tile of codes (contiguous in memory) ahead of the
@@ -588,64 +632,116 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
           }
         }
       }
-    } else if (ch < 2) {
-      // -------------------------------------------------------- MMA issue
-      constexpr uint32_t idS = idesc_f16(128, kAttnBN, false), idO = idesc_f16(128, DH, true);
-      const uint32_t tS = tmem + ch * kAttnBN, tO = tmem + 2 * kAttnBN + ch * DH;
-      const uint64_t dQ = sdesc_sw128(smem_u32(base + SL.q) + ch * NSUB * kSub, 16, 1024);
-      const uint64_t dK0 = sdesc_sw128(smem_u32(base + SL.k), 16, 1024);
-      const uint64_t dV0 = sdesc_sw128(smem_u32(base + SL.v), kSub, 1024);
-      int kt = 0, pt = 0, qi = 0;
+    } else if (warp == 15) {
+      // ------------------------------------ scales of the context tiles
+      // Lane g < 8: 16 keys.  A tile's scales go with its V slot: once P . V of
+      // the tile that had the slot before has run, its softmax is done.
+      int kt = 0, used0 = 0, used1 = 0;
       bool ok = true;
-      for (; ok && walk.next(ub, uk, sa, sb, L); kt += sb - sa) {
-        const int step = split ? 2 : 1, first = sa + (split ? ch : 0);
-        if (first >= sb) continue;
-        auto scores = [&](int i, int turn) -> bool {
-          const int t = kt + i - sa, slot = split ? ch : t & 1;
-          if (!mbar_wait_inline(&k_full[slot], (uint32_t)(split ? turn : t >> 1) & 1u, a.err,
-                                abort_flag, WHERE_ATTN_MMA))
-            return false;
-          tc_fence_after();
-          if (lane == 0) {
-            const uint64_t dK = dK0 + (uint64_t)((uint32_t)(slot * NSUB) * (kSub >> 4));
-#pragma unroll
-            for (int k = 0; k < DH / 16; ++k) {
-              const uint64_t off = (uint64_t)(((k >> 2) * kSub + (k & 3) * 32) >> 4);
-              umma_bf16_ss(tS, dQ + off, dK + off, idS, k > 0);
-            }
-            umma_commit(&s_full[ch]);
-            umma_commit(&k_empty[slot]);
-          }
-          __syncwarp();
-          return true;
+      while (ok && walk.next(ub, uk, sa, sb, L)) {
+        const size_t pair = (size_t)ub * a.Hkv + uk / a.n_qtiles;
+        const float* ksp = a.k_scale + pair * a.n_blocks;
+        const float* vsp = a.v_scale + pair * a.n_blocks;
+        float nk = 1.f, nw = 1.f;  // a tile ahead
+        auto load = [&](int tl) {
+          const int pos = (tl - 1) * kAttnBN + lane * 16;
+          const bool in = lane < 8 && tl > 0 && tl < sb && pos < L;
+          nk = in ? __ldg(ksp + (pos >> a.block_shift)) : 1.f;
+          nw = in ? __ldg(vsp + (pos >> a.block_shift)) : 1.f;
         };
-        ok = mbar_wait_inline(&q_full[ch], (uint32_t)qi & 1u, a.err, abort_flag, WHERE_ATTN_MMA);
-        if (ok) tc_fence_after();
-        if (ok) ok = scores(first, pt);
-        for (int i = first; ok && i < sb; i += step, ++pt) {
-          const int t = kt + i - sa, slot = split ? ch : t & 1;
-          if (!mbar_wait_inline(&p_full[ch], (uint32_t)pt & 1u, a.err, abort_flag, WHERE_ATTN_MMA) ||
-              !mbar_wait_inline(&v_full[slot], (uint32_t)(split ? pt : t >> 1) & 1u, a.err, abort_flag,
-                         WHERE_ATTN_MMA)) {
+        load(sa);
+        for (int tl = sa; tl < sb; ++tl, ++kt) {
+          const int slot = split ? (tl - sa) & 1 : kt & 1;
+          const uint32_t par = ((uint32_t)(slot ? used1++ : used0++) & 1u) ^ 1u;
+          ok = mbar_wait_inline(&v_empty[slot], par, a.err, abort_flag, WHERE_ATTN_PRODUCER);
+          if (!ok) break;
+          if (tl > 0 && lane < 8)
+            put_scales(scales + slot * 24, lane, nk, log2f(nw), 1.f / nw, &sc_full[slot]);
+          load(tl + 1);
+          __syncwarp();
+        }
+      }
+    } else if (warp == 12) {
+      // -------------------------------------------- S = Q . K^T, both chains
+      constexpr uint32_t idS = idesc_f16(128, kAttnBN, false);
+      const uint64_t dQ0 = sdesc_sw128(smem_u32(base + SL.q), 16, 1024);
+      const uint64_t dK0 = sdesc_sw128(smem_u32(base + SL.k), 16, 1024);
+      int kt = 0, n = 0, used0 = 0, used1 = 0;  // tiles, products, uses of each slot
+      int qs0 = 0, qs1 = 0;                     // segments of each chain
+      bool ok = true;
+      while (ok && walk.next(ub, uk, sa, sb, L)) {
+        for (int i = sa; ok && i < sb; ++i, ++kt) {
+          const int slot = split ? (i - sa) & 1 : kt & 1;
+          const uint32_t par = (uint32_t)(slot ? used1++ : used0++) & 1u;
+          if (!mbar_wait_inline(&k_full[slot], par, a.err, abort_flag, WHERE_ATTN_MMA)) {
             ok = false;
             break;
           }
-          tc_fence_after();
-          if (lane == 0) {
-            const int ksteps = (tile_keys(i, L, a.S) + 15) >> 4;
-            const uint64_t dV = dV0 + (uint64_t)((uint32_t)(slot * NSUB) * (kSub >> 4));
+          for (int c = split ? slot : 0; c < (split ? slot + 1 : 2); ++c, ++n) {
+            if (i == (split ? sa + c : sa) &&
+                !mbar_wait_inline(&q_full[c], (uint32_t)(c ? qs1++ : qs0++) & 1u, a.err,
+                                  abort_flag, WHERE_ATTN_MMA)) {
+              ok = false;
+              break;
+            }
+            if (n > 0 && !mbar_wait_inline(s_free, (uint32_t)(n - 1) & 1u, a.err, abort_flag,
+                                           WHERE_ATTN_MMA)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            if (elect_one()) {
+              const uint64_t dQ = dQ0 + (uint64_t)((uint32_t)(c * NSUB) * (kSub >> 4));
+              const uint64_t dK = dK0 + (uint64_t)((uint32_t)(slot * NSUB) * (kSub >> 4));
 #pragma unroll
-            for (int k = 0; k < kAttnBN / 16; ++k)
-              if (k < ksteps)
-                umma_bf16_ts(tO, tS + k * 8, dV + (uint64_t)(k * (2048 >> 4)), idO,
-                             (i > first || k > 0) ? 1u : 0u);
-            umma_commit(&v_empty[slot]);
-            if (i + step >= sb) umma_commit(&o_full[ch]);
+              for (int k = 0; k < DH / 16; ++k) {
+                const uint64_t off = (uint64_t)(((k >> 2) * kSub + (k & 3) * 32) >> 4);
+                umma_bf16_ss(tmem, dQ + off, dK + off, idS, k > 0);
+              }
+              umma_commit(&s_full[c]);
+              if (split || c == 1) umma_commit(&k_empty[slot]);
+            }
+            __syncwarp();
           }
-          __syncwarp();
-          if (i + step < sb) ok = scores(i + step, pt + 1);
         }
-        ++qi;
+      }
+    } else if (warp == 13) {
+      // ---------------------------------------------- O += P . V, both chains
+      constexpr uint32_t idO = idesc_f16(128, DH, true);
+      const uint64_t dV0 = sdesc_sw128(smem_u32(base + SL.v), kSub, 1024);
+      int kt = 0, used0 = 0, used1 = 0, pt0 = 0, pt1 = 0;
+      bool ok = true;
+      while (ok && walk.next(ub, uk, sa, sb, L)) {
+        for (int i = sa; ok && i < sb; ++i, ++kt) {
+          const int slot = split ? (i - sa) & 1 : kt & 1;
+          const uint32_t par = (uint32_t)(slot ? used1++ : used0++) & 1u;
+          const int ksteps = (tile_keys(i, L, a.S) + 15) >> 4;
+          if (!mbar_wait_inline(&v_full[slot], par, a.err, abort_flag, WHERE_ATTN_MMA)) {
+            ok = false;
+            break;
+          }
+          for (int c = split ? slot : 0; c < (split ? slot + 1 : 2); ++c) {
+            if (!mbar_wait_inline(&p_full[c], (uint32_t)(c ? pt1++ : pt0++) & 1u, a.err,
+                                  abort_flag, WHERE_ATTN_MMA)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            if (elect_one()) {
+              const uint32_t tP = tmem + kAttnBN + c * 64, tO = tmem + 2 * kAttnBN + c * DH;
+              const uint32_t more = i > (split ? sa + c : sa) ? 1u : 0u;
+              const uint64_t dV = dV0 + (uint64_t)((uint32_t)(slot * NSUB) * (kSub >> 4));
+#pragma unroll
+              for (int k = 0; k < kAttnBN / 16; ++k)
+                if (k < ksteps)
+                  umma_bf16_ts(tO, tP + k * 8, dV + (uint64_t)(k * (2048 >> 4)), idO,
+                               k > 0 ? 1u : more);
+              umma_commit(&pv_done[c]);
+              if (split || c == 1) umma_commit(&v_empty[slot]);
+            }
+            __syncwarp();
+          }
+        }
       }
     }
   }
@@ -654,7 +750,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
   __syncthreads();
   if (warp == 12) {
     tc_fence_after();
-    tmem_dealloc(tmem, kTmemCols);
+    tmem_dealloc(tmem, 512);
   }
 }
 

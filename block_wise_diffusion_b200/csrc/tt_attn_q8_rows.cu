@@ -217,8 +217,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_rows_kernel(const AttnQ8A
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
         const int pos = key0 + 16 * g;
-        nks[g] = pos < key_hi ? __ldg(ksp + pos / a.block) : 1.f;
-        nvs[g] = pos < key_hi ? __ldg(vsp + pos / a.block) : 1.f;
+        nks[g] = pos < key_hi ? __ldg(ksp + (pos >> a.block_shift)) : 1.f;
+        nvs[g] = pos < key_hi ? __ldg(vsp + (pos >> a.block_shift)) : 1.f;
       }
     };
     int key0 = key_lo + warp * kGroup;

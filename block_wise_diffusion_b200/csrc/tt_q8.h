@@ -48,7 +48,7 @@ cudaError_t launch_gemm_i8_linear(const CUtensorMap& tmA, const CUtensorMap& tmB
 // Units, query tiles and the partition of key tiles are those of the bf16
 // call; see tt_attn_q8.cuh for the schedule.
 struct AttnQ8Args {
-  int B, S, Hq, Hkv, dh, G, L_cap, block, n_blocks;
+  int B, S, Hq, Hkv, dh, G, L_cap, block_shift, n_blocks;  // 2^block_shift positions per scale
   const uint16_t *q, *k_blk, *v_blk;
   const uint8_t *k_ctx, *v_ctx;
   const float *k_scale, *v_scale;
