@@ -177,7 +177,7 @@ __device__ __forceinline__ void lds4f(uint32_t addr, float (&v)[4]) {
 // row sum.  kf: key scale, lw: log2 of the value scale, iw: its inverse.
 __device__ __forceinline__ void exps16(const uint32_t* s, float kf, float lw, float iw, float c_row,
                                        float m, float& l, uint32_t (&p)[8]) {
-  const float c = c_row * kf, off = lw - m;
+  const float c = kf, off = lw - m;
   const uint64_t c2 = pack2(c, c), o2 = pack2(off, off);
   uint64_t sum = 0;
 #pragma unroll
@@ -219,11 +219,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
   uint64_t* s_free = s_full + 2;         // S is in registers
   uint64_t* p_full = s_free + 1;         // [chain] P written, O corrected
   uint64_t* pv_done = p_full + 2;        // [chain] P . V done
-  uint64_t* k_full = pv_done + 2;        // [slot]
-  uint64_t* k_empty = k_full + kSlots;   // [slot]
-  uint64_t* v_full = k_empty + kSlots;
-  uint64_t* v_empty = v_full + kSlots;
-  uint64_t* sc_full = v_empty + kSlots;  // [slot]
+  uint64_t* full = pv_done + 2;          // [K, V][slot]
+  uint64_t* empty = full + 2 * kSlots;   // [K, V][slot]
+  uint64_t* sc_full = empty + 2 * kSlots;  // [slot]
   uint64_t* rk_full = sc_full + kSlots;  // [K, V] a tile of codes has landed
   uint64_t* rk_empty = rk_full + 2;      // [K, V] it has been converted
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(rk_empty + 2);
@@ -244,10 +242,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
       mbar_init(&rk_empty[c], kConv);
     }
     for (int s = 0; s < kSlots; ++s) {
-      mbar_init(&k_full[s], kConv);
-      mbar_init(&k_empty[s], 1);
-      mbar_init(&v_full[s], kConv);
-      mbar_init(&v_empty[s], 1);
+      for (int kv = 0; kv < 2; ++kv) {
+        mbar_init(&full[2 * kv + s], kConv);
+        mbar_init(&empty[2 * kv + s], 1);
+      }
       mbar_init(&sc_full[s], 8);
     }
     *abort_flag = 0;
@@ -306,19 +304,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
         // segment's last S of this chain has been waited for below.
         float c_row = 0.f;
         {
+          const uint4 zero = make_uint4(0, 0, 0, 0);
+          // all of the row's loads in flight at once
+          const uint4* src = reinterpret_cast<const uint4*>(a.q + qrow * DH);
           uint4 x[DH / 8];
           uint32_t mx = 0;
 #pragma unroll
-          for (int i = 0; i < DH / 8; ++i)
-            x[i] = valid ? *reinterpret_cast<const uint4*>(a.q + qrow * DH + i * 8)
-                         : make_uint4(0, 0, 0, 0);
+          for (int i = 0; i < DH / 8; ++i) x[i] = valid ? src[i] : zero;
 #pragma unroll
-          for (int i = 0; i < DH / 8; ++i) {
-            mx = __vmaxu2(mx, x[i].x & 0x7FFF7FFFu);
-            mx = __vmaxu2(mx, x[i].y & 0x7FFF7FFFu);
-            mx = __vmaxu2(mx, x[i].z & 0x7FFF7FFFu);
-            mx = __vmaxu2(mx, x[i].w & 0x7FFF7FFFu);
-          }
+          for (int i = 0; i < DH / 8; ++i) mx = absmax_bf16x8(mx, x[i]);
           const int e = norm_exp(max(mx & 0xFFFFu, mx >> 16));
           const float f = pow2i(-e);
           c_row = a.scale_log2 * pow2i(e);
@@ -338,6 +332,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
             break;
           }
           const uint32_t sc = smem_u32(scales + ts * 24);
+          float kf[8], lw[8], iw[8];
+          lds4f(sc, *reinterpret_cast<float(*)[4]>(&kf[0]));
+          lds4f(sc + 16, *reinterpret_cast<float(*)[4]>(&kf[4]));
+          lds4f(sc + 32, *reinterpret_cast<float(*)[4]>(&lw[0]));
+          lds4f(sc + 48, *reinterpret_cast<float(*)[4]>(&lw[4]));
+          lds4f(sc + 64, *reinterpret_cast<float(*)[4]>(&iw[0]));
+          lds4f(sc + 80, *reinterpret_cast<float(*)[4]>(&iw[4]));
+#pragma unroll
+          for (int g = 0; g < 8; ++g) kf[g] *= c_row;
           if (!mbar_wait_inline(&s_full[ch], (uint32_t)pt & 1u, a.err, abort_flag,
                                 WHERE_ATTN_SOFTMAX)) {
             ok = false;
@@ -355,7 +358,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
           float alpha = 1.f;
           bool need = false;
           uint32_t p0[8], p1[8];
-          float kf[4], lw[4], iw[4];
           const int nv = tile_keys(i, L, a.S);
           if (nv < kAttnBN) {
 #pragma unroll
@@ -364,13 +366,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
           }
           float mx = -INFINITY;
 #pragma unroll
-          for (int g = 0; g < 8; g += 4) {
-            float kf[4], lw[4];
-            lds4f(sc + 4 * g, kf);
-            lds4f(sc + 32 + 4 * g, lw);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint32_t* x = s + 16 * (g + k);
+          for (int g = 0; g < 8; ++g) {
+            {
+              const uint32_t* x = s + 16 * g;
               float y0 = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
               float y1 = fmaxf(__uint_as_float(x[2]), __uint_as_float(x[3]));
 #pragma unroll
@@ -378,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
                 y0 = fmax3(y0, __uint_as_float(x[j]), __uint_as_float(x[j + 1]));
                 y1 = fmax3(y1, __uint_as_float(x[j + 2]), __uint_as_float(x[j + 3]));
               }
-              mx = fmaxf(mx, fmaf(fmaxf(y0, y1), c_row * kf[k], lw[k]));
+              mx = fmaxf(mx, fmaf(fmaxf(y0, y1), kf[g], lw[g]));
             }
           }
           need = mx > m + kRescale;
@@ -387,9 +385,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
             m = mx;
           }
           l *= alpha;
-          lds4f(sc, kf);
-          lds4f(sc + 32, lw);
-          lds4f(sc + 64, iw);
           exps16(s, kf[0], lw[0], iw[0], c_row, m, l, p0);
           exps16(s + 16, kf[1], lw[1], iw[1], c_row, m, l, p1);
           // P and O are the tensor core's until P . V of the turn before has run
@@ -419,16 +414,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
           tmem_st8(tP + 16, p0);
           exps16(s + 48, kf[3], lw[3], iw[3], c_row, m, l, p1);
           tmem_st8(tP + 24, p1);
-          lds4f(sc + 16, kf);
-          lds4f(sc + 48, lw);
-          lds4f(sc + 80, iw);
-          exps16(s + 64, kf[0], lw[0], iw[0], c_row, m, l, p0);
+          exps16(s + 64, kf[4], lw[4], iw[4], c_row, m, l, p0);
           tmem_st8(tP + 32, p0);
-          exps16(s + 80, kf[1], lw[1], iw[1], c_row, m, l, p1);
+          exps16(s + 80, kf[5], lw[5], iw[5], c_row, m, l, p1);
           tmem_st8(tP + 40, p1);
-          exps16(s + 96, kf[2], lw[2], iw[2], c_row, m, l, p0);
+          exps16(s + 96, kf[6], lw[6], iw[6], c_row, m, l, p0);
           tmem_st8(tP + 48, p0);
-          exps16(s + 112, kf[3], lw[3], iw[3], c_row, m, l, p1);
+          exps16(s + 112, kf[7], lw[7], iw[7], c_row, m, l, p1);
           tmem_st8(tP + 56, p1);
           tmem_wait_st();
           tc_fence_before();
@@ -489,25 +481,30 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
     const int half = (tid >> 2) & 1;
     const int row0 = DH == 64 ? tid >> 2 : ((tid >> 4) << 1) + half;
     const int col = DH == 64 ? tid & 3 : (tid & 3) + 4 * (half ^ ((tid >> 3) & 1));
-    const uint32_t sK = smem_u32(base + SL.k), sV = smem_u32(base + SL.v);
-    const uint32_t rK = smem_u32(base + SL.raw), rV = rK + kAttnBN * DH;
+    const uint32_t sK = smem_u32(base + SL.k), rK = smem_u32(base + SL.raw);  // V behind K
     auto convert = [&](uint32_t src, uint32_t dst, int nv) {
-      uint4 v[NV];
+      // rows 32 (dh 64) or 16 apart: the swizzle (row & 7) is the same for all
+      const uint32_t d0 = dst + chunk_at(row0, 2 * col), d1 = dst + chunk_at(row0, 2 * col + 1);
+      const uint32_t s0 = src + row0 * DH + col * 16;
+#pragma unroll 1
+      for (int i0 = 0; i0 < NV; i0 += 4) {
+        uint4 v[4];
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
-        v[i] = lds128(src + (row0 + i * (kConv * 16 / DH)) * DH + col * 16);
+        for (int i = 0; i < 4; ++i) v[i] = lds128(s0 + (i0 + i) * (kConv * 16));
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int row = row0 + i * (kConv * 16 / DH);
-        uint4 x = v[i];
-        if (row >= nv) x = make_uint4(0, 0, 0, 0);  // behind the context: zeros
-        uint32_t w[8];
-        codes4<TYPE>(x.x, w[0], w[1]);
-        codes4<TYPE>(x.y, w[2], w[3]);
-        codes4<TYPE>(x.z, w[4], w[5]);
-        codes4<TYPE>(x.w, w[6], w[7]);
-        sts128(dst + chunk_at(row, 2 * col), w[0], w[1], w[2], w[3]);
-        sts128(dst + chunk_at(row, 2 * col + 1), w[4], w[5], w[6], w[7]);
+        for (int i = 0; i < 4; ++i) {
+          const int row = row0 + (i0 + i) * (kConv * 16 / DH);
+          uint4 x = v[i];
+          if (row >= nv) x = make_uint4(0, 0, 0, 0);  // behind the context: zeros
+          uint32_t w[8];
+          codes4<TYPE>(x.x, w[0], w[1]);
+          codes4<TYPE>(x.y, w[2], w[3]);
+          codes4<TYPE>(x.z, w[4], w[5]);
+          codes4<TYPE>(x.w, w[6], w[7]);
+          const uint32_t at = (uint32_t)(i0 + i) * (kConv * 16 / DH) * 128;
+          sts128(d0 + at, w[0], w[1], w[2], w[3]);
+          sts128(d1 + at, w[4], w[5], w[6], w[7]);
+        }
       }
     };
     // The block's own rows [S, Hkv, dh] (bf16) by a power of two in fp16
@@ -521,10 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
         const int row = r0 + i * (kConv / (DH / 8));
         if (row < a.S) {
           const uint4 x = *reinterpret_cast<const uint4*>(p + (size_t)row * a.Hkv * DH + c0 * 8);
-          mx = __vmaxu2(mx, x.x & 0x7FFF7FFFu);
-          mx = __vmaxu2(mx, x.y & 0x7FFF7FFFu);
-          mx = __vmaxu2(mx, x.z & 0x7FFF7FFFu);
-          mx = __vmaxu2(mx, x.w & 0x7FFF7FFFu);
+          mx = absmax_bf16x8(mx, x);
         }
       }
       mx = __reduce_max_sync(0xffffffffu, max(mx & 0xFFFFu, mx >> 16));
@@ -555,40 +549,34 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
         // has one reader that sees its phases in order)
         const int slot = split ? (tl - sa) & 1 : kt & 1;
         const uint32_t par = ((uint32_t)(slot ? used1++ : used0++) & 1u) ^ 1u;
-        const uint32_t dK = sK + slot * NSUB * kSub, dV = sV + slot * NSUB * kSub;
         const int nv = tile_keys(tl, L, a.S);
-        if ((tl > 0 && !mbar_wait_inline(&rk_full[0], (uint32_t)raw & 1u, a.err, abort_flag,
-                                         WHERE_ATTN_PRODUCER)) ||
-            !mbar_wait_inline(&k_empty[slot], par, a.err, abort_flag, WHERE_ATTN_PRODUCER)) {
-          ok = false;
-          break;
+        int ek = 0;
+#pragma unroll 1
+        for (int kv = 0; kv < 2; ++kv) {  // K, then V
+          if ((tl > 0 && !mbar_wait_inline(&rk_full[kv], (uint32_t)raw & 1u, a.err, abort_flag,
+                                           WHERE_ATTN_PRODUCER)) ||
+              !mbar_wait_inline(&empty[2 * kv + slot], par, a.err, abort_flag,
+                                WHERE_ATTN_PRODUCER)) {
+            ok = false;
+            break;
+          }
+          const uint32_t dst = sK + (kv * kSlots + slot) * NSUB * kSub;
+          if (tl == 0) {
+            const int e = block_rows((kv ? a.v_blk : a.k_blk) +
+                                         ((size_t)ub * a.S * a.Hkv + ug) * DH, dst, kv);
+            // the block's scales; V's slot, once free, frees the scales' too
+            if (kv == 1 && tid < 8)
+              put_scales(scales + slot * 24, tid, pow2i(ek), (float)e, pow2i(-e), &sc_full[slot]);
+            ek = e;
+          } else {
+            convert(rK + kv * kAttnBN * DH, dst, nv);
+            mbar_arrive(&rk_empty[kv]);
+            raw += kv;
+          }
+          fence_proxy_async_smem();
+          mbar_arrive(&full[2 * kv + slot]);
         }
-        int ek = 0, ev = 0;
-        if (tl == 0) {
-          ek = block_rows(a.k_blk + ((size_t)ub * a.S * a.Hkv + ug) * DH, dK, 0);
-        } else {
-          convert(rK, dK, nv);
-          mbar_arrive(&rk_empty[0]);
-        }
-        fence_proxy_async_smem();
-        mbar_arrive(&k_full[slot]);
-        if ((tl > 0 && !mbar_wait_inline(&rk_full[1], (uint32_t)raw & 1u, a.err, abort_flag,
-                                         WHERE_ATTN_PRODUCER)) ||
-            !mbar_wait_inline(&v_empty[slot], par, a.err, abort_flag, WHERE_ATTN_PRODUCER)) {
-          ok = false;
-          break;
-        }
-        if (tl == 0) {
-          ev = block_rows(a.v_blk + ((size_t)ub * a.S * a.Hkv + ug) * DH, dV, 1);
-          if (tid < 8) put_scales(scales + slot * 24, tid, pow2i(ek), (float)ev, pow2i(-ev), &sc_full[slot]);
-        }
-        if (tl > 0) {
-          convert(rV, dV, nv);
-          mbar_arrive(&rk_empty[1]);
-          ++raw;
-        }
-        fence_proxy_async_smem();
-        mbar_arrive(&v_full[slot]);
+        if (!ok) break;
       }
     }
   } else {
@@ -653,7 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
         for (int tl = sa; tl < sb; ++tl, ++kt) {
           const int slot = split ? (tl - sa) & 1 : kt & 1;
           const uint32_t par = ((uint32_t)(slot ? used1++ : used0++) & 1u) ^ 1u;
-          ok = mbar_wait_inline(&v_empty[slot], par, a.err, abort_flag, WHERE_ATTN_PRODUCER);
+          ok = mbar_wait_inline(&empty[2 + slot], par, a.err, abort_flag, WHERE_ATTN_PRODUCER);
           if (!ok) break;
           if (tl > 0 && lane < 8)
             put_scales(scales + slot * 24, lane, nk, log2f(nw), 1.f / nw, &sc_full[slot]);
@@ -673,7 +661,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
         for (int i = sa; ok && i < sb; ++i, ++kt) {
           const int slot = split ? (i - sa) & 1 : kt & 1;
           const uint32_t par = (uint32_t)(slot ? used1++ : used0++) & 1u;
-          if (!mbar_wait_inline(&k_full[slot], par, a.err, abort_flag, WHERE_ATTN_MMA)) {
+          if (!mbar_wait_inline(&full[slot], par, a.err, abort_flag, WHERE_ATTN_MMA)) {
             ok = false;
             break;
           }
@@ -699,7 +687,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
                 umma_bf16_ss(tmem, dQ + off, dK + off, idS, k > 0);
               }
               umma_commit(&s_full[c]);
-              if (split || c == 1) umma_commit(&k_empty[slot]);
+              if (split || c == 1) umma_commit(&empty[slot]);
             }
             __syncwarp();
           }
@@ -716,7 +704,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
           const int slot = split ? (i - sa) & 1 : kt & 1;
           const uint32_t par = (uint32_t)(slot ? used1++ : used0++) & 1u;
           const int ksteps = (tile_keys(i, L, a.S) + 15) >> 4;
-          if (!mbar_wait_inline(&v_full[slot], par, a.err, abort_flag, WHERE_ATTN_MMA)) {
+          if (!mbar_wait_inline(&full[2 + slot], par, a.err, abort_flag, WHERE_ATTN_MMA)) {
             ok = false;
             break;
           }
@@ -737,7 +725,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
                   umma_bf16_ts(tO, tP + k * 8, dV + (uint64_t)(k * (2048 >> 4)), idO,
                                k > 0 ? 1u : more);
               umma_commit(&pv_done[c]);
-              if (split || c == 1) umma_commit(&v_empty[slot]);
+              if (split || c == 1) umma_commit(&empty[2 + slot]);
             }
             __syncwarp();
           }
@@ -754,60 +742,74 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
   }
 }
 
-// Thread = (unit, query row, 4 columns): the unit's segment partials (two per
-// segment where the chains split the tiles) into the bf16 output, in one
-// pass with a running maximum.
+// The segment partials of a unit that several CTAs hold (two per segment where
+// the chains split the tiles) into the bf16 output.  Block = (unit, 32 query
+// rows, 1 / parts of the columns), lane = row, NG groups of 4 columns to a
+// warp, whose loads are 512 contiguous bytes.  One pass with a running maximum;
+// the loads of KB records are in flight together, for latency is all there is.
+template <int NG, int KB>
 __global__ void __launch_bounds__(256) attn_q8_merge_kernel(const AttnQ8Args a) {
   griddep_launch();
   griddep_wait();
-  const int ngrp = a.dh / 4, rows = a.halves * 128;
-  const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-  const int row = (int)(i % rows);
-  const int grp = (int)(i / rows % ngrp);
-  const long long u = i / rows / ngrp;
-  if (u >= a.units) return;
-  const int h = row >> 7, r = row & 127;
-  if (r >= a.rows_per_half) return;
+  const int row_blocks = a.halves * 4, ngrp = a.dh / 4, parts = ngrp / (8 * NG);
+  const int part = blockIdx.x % parts, rb = blockIdx.x / parts % row_blocks;
+  const int u = blockIdx.x / (parts * row_blocks);
   const int2 uc = unit_ctas(a, u);
-  const int per = a.halves == 1 ? 2 : 1;  // partials per segment
+  const int per = a.halves == 1 ? 2 : 1;  // records per segment
   if (per == 1 && uc.x == uc.y) return;   // written by its CTA
+  const int lane = threadIdx.x & 31, row = rb * 32 + lane, h = row >> 7, r = row & 127;
+  if (rb * 32 - h * 128 >= a.rows_per_half) return;  // no rows in this block
   const int n = (uc.y - uc.x + 1) * per;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float den = 0.f, mrun = -INFINITY;
-  for (int c0 = 0; c0 < n; c0 += 4) {
-    float2 ml[4];
-    float4 o[4];
+  const size_t slot0 = (size_t)u + uc.x;
+  const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + slot0 * 256;
+  const float4* po = reinterpret_cast<const float4*>(a.part_o) + slot0 * ngrp * 256;
+  // record c: row of the segment's 256 (its chain's 128 where the chains split)
+  auto at = [&](int c) { return per == 2 ? (c & 1) * 128 + r : row; };
+  auto rec = [&](int c) { return (size_t)(per == 2 ? c >> 1 : c); };
+  const int g0 = (part * 8 + (threadIdx.x >> 5)) * NG;
+  float mx = -INFINITY, den = 0.f;
+  float4 acc[NG];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int c = c0 + k;
-      const size_t slot = (size_t)u + uc.x + c / per;
-      const size_t at = per == 2 ? (size_t)((c & 1) * 128 + r) : (size_t)row;
-      ml[k] = c < n ? __ldcg(reinterpret_cast<const float2*>(a.part_ml + (slot * 256 + at) * 2))
-                    : make_float2(-INFINITY, 0.f);
-      o[k] = c < n ? __ldcg(reinterpret_cast<const float4*>(a.part_o + ((slot * ngrp + grp) * 256 + at) * 4))
-                   : make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int g = 0; g < NG; ++g) acc[g] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+  for (int c0 = 0; c0 < n; c0 += KB) {
+    float2 x[KB];
+    float4 o[KB][NG];
+#pragma unroll
+    for (int k = 0; k < KB; ++k) {
+      const int c = min(c0 + k, n - 1);
+      x[k] = __ldg(ml + rec(c) * 256 + at(c));
+#pragma unroll
+      for (int g = 0; g < NG; ++g) o[k][g] = __ldcg(po + (rec(c) * ngrp + g0 + g) * 256 + at(c));
     }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (ml[k].y == 0.f) continue;  // no keys: its O was never written
-      const float mn = ml[k].x > mrun ? ml[k].x : mrun;
-      const float w0 = ex2(mrun - mn), w1 = ex2(ml[k].x - mn);
-      mrun = mn;
-      den = fmaf(den, w0, ml[k].y * w1);
-      acc.x = fmaf(acc.x, w0, o[k].x * w1);
-      acc.y = fmaf(acc.y, w0, o[k].y * w1);
-      acc.z = fmaf(acc.z, w0, o[k].z * w1);
-      acc.w = fmaf(acc.w, w0, o[k].w * w1);
+    for (int k = 0; k < KB; ++k) {
+      // past the last record, or one without keys (its output was never written)
+      if (c0 + k >= n || x[k].y == 0.f) continue;
+      const float mn = x[k].x > mx ? x[k].x : mx;
+      const float f0 = ex2(mx - mn), f1 = ex2(x[k].x - mn);
+      mx = mn;
+      den = fmaf(den, f0, x[k].y * f1);
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        acc[g].x = fmaf(acc[g].x, f0, o[k][g].x * f1);
+        acc[g].y = fmaf(acc[g].y, f0, o[k][g].y * f1);
+        acc[g].z = fmaf(acc[g].z, f0, o[k][g].z * f1);
+        acc[g].w = fmaf(acc[g].w, f0, o[k][g].w * f1);
+      }
     }
   }
   const float inv = 1.f / den;
-  const int qt = (int)(u % a.n_qtiles);
-  const long long pair = u / a.n_qtiles;
-  const long long b = pair / a.Hkv, g = pair % a.Hkv;
+  if (r >= a.rows_per_half) return;
+  const int U = a.Hkv * a.n_qtiles;
+  const int b = u / U, uk = u - b * U, ug = uk / a.n_qtiles, qt = uk - ug * a.n_qtiles;
   const int s = qt * a.halves * a.s_per_half + h * a.s_per_half + r / a.G;
-  const int head = (int)g * a.G + r % a.G;
-  *reinterpret_cast<uint2*>(a.out + ((size_t)(b * a.S + s) * a.Hq + head) * a.dh + grp * 4) =
-      make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+  uint16_t* dst = a.out + (((size_t)b * a.S + s) * a.Hq + ug * a.G + r % a.G) * a.dh + g0 * 4;
+#pragma unroll
+  for (int g = 0; g < NG; ++g)
+    *reinterpret_cast<uint2*>(dst + 4 * g) =
+        make_uint2(pack_bf16x2(acc[g].x * inv, acc[g].y * inv),
+                   pack_bf16x2(acc[g].z * inv, acc[g].w * inv));
 }
 
 template <int TYPE, int DH>
@@ -829,9 +831,15 @@ cudaError_t launch_attn_q8(const AttnQ8Args& a, int type, cudaStream_t st) {
 }
 
 cudaError_t launch_attn_q8_merge(const AttnQ8Args& a, cudaStream_t st) {
-  const long long threads = (long long)a.units * a.halves * 128 * (a.dh / 4);
-  return launch_k(attn_q8_merge_kernel, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, st,
-                  a);
+  // Few units (many records each): a quarter (dh 128) or half of a row to a
+  // block, so that the whole GPU reads, and ten records at a time.  Many units
+  // have two or three records: whole rows, which share the weights' arithmetic.
+  const int blocks = a.units * a.halves * 4;
+  if (blocks < 4 * num_sms())
+    return launch_k(attn_q8_merge_kernel<1, 10>, dim3(blocks * (a.dh / 32)), dim3(256), 0, st, a);
+  if (a.dh == 64)
+    return launch_k(attn_q8_merge_kernel<2, 4>, dim3(blocks), dim3(256), 0, st, a);
+  return launch_k(attn_q8_merge_kernel<4, 3>, dim3(blocks), dim3(256), 0, st, a);
 }
 
 }  // namespace tt

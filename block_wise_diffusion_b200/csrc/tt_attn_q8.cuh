@@ -7,7 +7,9 @@
 // sums over the B sequences alone, and every CTA computes them itself from
 // ctx_len instead of waiting for a planning kernel.  CTA c takes the tiles
 // [c T / P, (c + 1) T / P) of the T tiles; its part of unit u (a segment) has
-// the partial record u + c, which no other segment has.
+// the partial record u + c, which no other segment has.  T < 2^31 is checked
+// on the host: the arithmetic is 32-bit, and the whole prologue small, because
+// every launch pays for it.
 #pragma once
 #include "tt_q8.h"
 #include "tt_ptx.cuh"
@@ -17,10 +19,10 @@ namespace tt {
 // One position in the tile sequence and what is left of the CTA's range.
 struct TileWalk {
   const int* ctx_len;
-  long long left;  // tiles of the range not yet handed out
-  int L_cap, U;    // units per sequence
-  int b, k;        // sequence, unit within it
-  int off;         // tile within the unit
+  int left;      // tiles of the range not yet handed out
+  int L_cap, U;  // units per sequence
+  int b, k;      // sequence, unit within it
+  int off;       // tile within the unit
   // The next segment: unit (b, k), local tiles [a, e), context length L.
   __device__ __forceinline__ bool next(int& sb, int& sk, int& a, int& e, int& L) {
     if (left <= 0) return false;
@@ -29,7 +31,7 @@ struct TileWalk {
     sb = b;
     sk = k;
     a = off;
-    e = (int)min((long long)n, off + left);
+    e = min(n, off + left);
     left -= e - a;
     off = 0;
     if (++k == U) {
@@ -41,10 +43,19 @@ struct TileWalk {
 };
 
 struct PlanSmem {
-  long long warp_tot[32];
-  long long total, pre;
-  int b, bad;
+  int warp_tot[32];
+  int b, pre;
 };
+
+// First tile of CTA c, floor(c T / P) (P <= 1024: no product leaves 32 bits),
+// and the CTA that holds tile t.
+__device__ __forceinline__ int cta_first(int c, int T, int P) {
+  const int base = T / P;
+  return c * base + c * (T - base * P) / P;
+}
+__device__ __forceinline__ int tile_cta(int t, int T, int P) {
+  return (int)(((long long)(t + 1) * P - 1) / T);
+}
 
 // Every thread of the CTA: the CTA's walk.  CTA 0 also stores the prefix sums
 // over sequences for the merge, and starts the error word (an out-of-range
@@ -59,43 +70,38 @@ __device__ __forceinline__ TileWalk plan_walk(const AttnQ8Args& a, PlanSmem& sm)
     bad |= L < 0 || L > a.L_cap;
     return 1 + (min(max(L, 0), a.L_cap) + kAttnBN - 1) / kAttnBN;
   };
-  long long sum = 0;
-  int bad = 0;
+  int sum = 0, bad = 0;
+#pragma unroll 1
   for (int b = b0; b < b1; ++b) sum += tiles(b, bad);
-  long long incl = sum;
+  int incl = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+    const int y = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += y;
   }
   if (lane == 31) sm.warp_tot[warp] = incl;
   bad = __syncthreads_or(bad);
-  long long before = 0, total = 0;
-  for (int w = 0; w < NT / 32; ++w) {
-    const long long x = sm.warp_tot[w];
-    before += w < warp ? x : 0;
-    total += x;
-  }
-  const int U = a.Hkv * a.n_qtiles;
-  const long long T = total * U;
-  const long long lo = (long long)blockIdx.x * T / a.n_ctas;
-  const long long hi = (long long)(blockIdx.x + 1) * T / a.n_ctas;
-  long long pre = before + incl - sum;
+  const int mine = lane < NT / 32 ? sm.warp_tot[lane] : 0;
+  const int total = __reduce_add_sync(0xffffffffu, mine);
+  int pre = incl - sum + __reduce_add_sync(0xffffffffu, lane < warp ? mine : 0);
+  const int U = a.Hkv * a.n_qtiles, T = total * U;
+  const int lo = cta_first(blockIdx.x, T, a.n_ctas);
   if (blockIdx.x == 0) {
-    long long p = pre;
-    int x = 0;
+    int p = pre, x = 0;
+#pragma unroll 1
     for (int b = b0; b < b1; ++b) {
-      a.seq_start[b] = (int)p;
+      a.seq_start[b] = p;
       p += tiles(b, x);
     }
     if (tid == 0) {
-      a.seq_start[a.B] = (int)total;
+      a.seq_start[a.B] = total;
       a.err[0] = bad ? (int)TT_ERR_INVALID_ARG : 0;
       a.err[1] = 0;
     }
   }
   if (lo >= pre * U && lo < (pre + sum) * U) {  // exactly one thread
     int b = b0, x = 0;
+#pragma unroll 1
     for (;; ++b) {
       const int n = tiles(b, x);
       if (lo < (pre + n) * U) break;
@@ -109,11 +115,11 @@ __device__ __forceinline__ TileWalk plan_walk(const AttnQ8Args& a, PlanSmem& sm)
   w.ctx_len = a.ctx_len;
   w.L_cap = a.L_cap;
   w.U = U;
-  w.left = hi - lo;
+  w.left = cta_first(blockIdx.x + 1, T, a.n_ctas) - lo;
   w.b = sm.b;
   int x = 0;
   const int n = tiles(w.b, x);
-  const int rem = (int)(lo - sm.pre * U);
+  const int rem = lo - sm.pre * U;
   w.k = rem / n;
   w.off = rem - w.k * n;
   return w;
@@ -126,13 +132,12 @@ __device__ __forceinline__ int tile_keys(int t, int L, int S) {
 
 // The CTAs that hold a unit's tiles (all of [x, y] have a record, an empty
 // range inside the unit an empty one).
-__device__ __forceinline__ int2 unit_ctas(const AttnQ8Args& a, long long u) {
+__device__ __forceinline__ int2 unit_ctas(const AttnQ8Args& a, int u) {
   const int U = a.Hkv * a.n_qtiles;
-  const int b = (int)(u / U), k = (int)(u - (long long)b * U);
-  const int p0 = a.seq_start[b], n = a.seq_start[b + 1] - p0;
-  const long long T = (long long)a.seq_start[a.B] * U;
-  const long long s0 = (long long)p0 * U + (long long)k * n, s1 = s0 + n;
-  return make_int2((int)(((s0 + 1) * a.n_ctas - 1) / T), (int)((s1 * a.n_ctas - 1) / T));
+  const int b = u / U, k = u - b * U;
+  const int p0 = a.seq_start[b], n = a.seq_start[b + 1] - p0, T = a.seq_start[a.B] * U;
+  const int s0 = p0 * U + k * n;
+  return make_int2(tile_cta(s0, T, a.n_ctas), tile_cta(s0 + n - 1, T, a.n_ctas));
 }
 
 // 2^e, e in [-126, 127]

@@ -370,10 +370,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_rows_kernel(const AttnQ8A
 __global__ void __launch_bounds__(128) attn_q8_rows_merge_kernel(const AttnQ8Args a) {
   griddep_launch();
   griddep_wait();
-  const long long u = blockIdx.x;
+  const int u = blockIdx.x;
   const int2 uc = unit_ctas(a, u);
   if (uc.x == uc.y) return;  // written by its CTA
-  const int b = (int)(u / a.Hkv), g = (int)(u - (long long)b * a.Hkv), dv = a.dh / 4;
+  const int b = u / a.Hkv, g = u - b * a.Hkv, dv = a.dh / 4;
   for (int i = threadIdx.x; i < a.rows_per_half * dv; i += 128) {
     const int r = i / dv, v = i - r * dv;
     float mr = -INFINITY, den = 0.f;
