@@ -281,8 +281,8 @@ tt_status tt_append_ctx_q8(const tt_dims* d, const tt_q8* f, int32_t n, const in
   a.v_scale = v_scale;
   a.ctx_len = ctx_len;
   a.err = static_cast<int*>(ws);
-  Q8_CUDA(cudaMemsetAsync(ws, 0, kCtrlBytes, st));
   Q8_LAUNCH(TT_K_APPEND_Q8, st, launch_append_q8(a, f->type, st));
+  Q8_LAUNCH(TT_K_APPEND_Q8, st, launch_append_q8_len(a, st));
   return TT_OK;
 }
 

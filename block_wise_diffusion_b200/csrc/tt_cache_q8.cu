@@ -9,7 +9,11 @@ namespace tt {
 
 namespace {
 
-constexpr int kAppendThreads = 256;
+// A thread holds kVec vectors of 8 values of one cache block, so a block of
+// block * dh values takes block * dh / 32 threads: 32 (16 x 64) to 512 (128 x
+// 128).  A CTA has at least 128 threads, several blocks where they are small.
+constexpr int kVec = 4;
+constexpr int append_block_threads(int block_values) { return block_values / (8 * kVec); }
 
 // How many rows sequence b gets, or -1 when its lengths are out of range.
 __device__ __forceinline__ int append_rows(const AppendQ8Args& a, int b, int L) {
@@ -17,92 +21,109 @@ __device__ __forceinline__ int append_rows(const AppendQ8Args& a, int b, int L) 
   return (m < 0 || m > a.n || L < 0 || L > a.L_cap - m) ? -1 : m;
 }
 
-// CTA (b, g, K or V, i), i fastest: the i-th cache block that sequence b's new
-// rows may touch, counted from the block that holds its end.  A thread holds vectors
-// of 8 values (at most 8: a block has at most 128 x 128 values).
-template <int TYPE>
-__global__ void __launch_bounds__(kAppendThreads) append_q8_kernel(const AppendQ8Args a) {
+// Item (b, g, K or V, i), i fastest: the i-th cache block that sequence b's new
+// rows may touch, counted from the block that holds its end.  NT: threads of a
+// block.
+template <int TYPE, int NT>
+__global__ void __launch_bounds__(NT < 128 ? 128 : NT) append_q8_kernel(const AppendQ8Args a) {
+  constexpr int kCta = NT < 128 ? 128 : NT;
   griddep_launch();
   griddep_wait();
-  __shared__ uint32_t red[kAppendThreads / 32];
+  __shared__ uint32_t red[kCta / 32];
   const int nb = (a.n + a.block - 1) / a.block + 1;
-  const int pair = blockIdx.x / nb, bi = blockIdx.x - pair * nb;
+  const int tid = threadIdx.x % NT;
+  const unsigned item = blockIdx.x * (kCta / NT) + threadIdx.x / NT;
+  const int pair = (int)(item / nb), bi = (int)(item - (unsigned)pair * nb);
   const int is_v = pair & 1, b = (pair >> 1) / a.Hkv, g = (pair >> 1) - b * a.Hkv;
-  const int L = a.ctx_len[b];
-  const int m = append_rows(a, b, L);
-  if (m < 0) {
-    if (threadIdx.x == 0 && bi == 0 && g == 0 && is_v == 0)
-      atomicCAS(a.err, 0, (int)TT_ERR_INVALID_ARG);
-    return;
+  int L = 0, m = 0;
+  if (b < a.B) {
+    L = a.ctx_len[b];
+    m = append_rows(a, b, L);
   }
   const int blk = L / a.block + bi;
   const long long p0 = (long long)blk * a.block;  // first position of the block
-  if (m == 0 || p0 >= (long long)L + m) return;
-  const int n_old = max(0, (int)(L - p0));         // older rows in the block
-  const int n_end = (int)min((long long)a.block, L + m - p0);
-  const int dv = a.dh >> 3;                        // vectors per row
-  const int lo = n_old * dv, hi = n_end * dv;      // new vectors of the block
+  const bool mine = m > 0 && p0 < (long long)L + m;
+  if (kCta == NT && !mine) return;
+  const int n_old = mine ? max(0, (int)(L - p0)) : 0;  // older rows in the block
+  const int n_end = mine ? (int)min((long long)a.block, L + m - p0) : 0;
+  const int dv_log = a.dh == 64 ? 3 : 4;              // vectors per row: 8 or 16
+  const int lo = n_old << dv_log, hi = n_end << dv_log;  // new vectors of the block
   const uint16_t* src = (is_v ? a.v_new : a.k_new) + (long long)b * a.stride_b +
                         (long long)g * a.stride_h + (p0 - L) * a.stride_t;
-  uint8_t* dst = (is_v ? a.v_ctx : a.k_ctx) + ((long long)(b * a.Hkv + g) * a.L_cap + p0) * a.dh;
-  float* sp = (is_v ? a.v_scale : a.k_scale) + (long long)(b * a.Hkv + g) * a.n_blocks + blk;
-
-  uint4 x[8];
+  uint4 x[kVec];
   uint32_t mx = 0;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const int i = lo + k * kAppendThreads + threadIdx.x;
+  for (int k = 0; k < kVec; ++k) {
+    const int i = lo + k * NT + tid;
     if (i < hi) {
-      const int t = i / dv;
-      x[k] = *reinterpret_cast<const uint4*>(src + (long long)t * a.stride_t + (i - t * dv) * 8);
+      const int t = i >> dv_log;
+      x[k] = *reinterpret_cast<const uint4*>(src + (long long)t * a.stride_t +
+                                             (i - (t << dv_log)) * 8);
       mx = absmax8(mx, x[k]);
     }
   }
   mx = __reduce_max_sync(0xffffffffu, absmax_fold(mx));
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = mx;
-  __syncthreads();
-  mx = 0;
+  if constexpr (NT > 32) {
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = mx;
+    __syncthreads();
+    const int w0 = threadIdx.x / NT * (NT / 32);
+    mx = red[w0];
 #pragma unroll
-  for (int w = 0; w < kAppendThreads / 32; ++w) mx = max(mx, red[w]);
-  float s = q8_scale<TYPE>(mx);
-  if (n_old > 0) {
-    const float s_old = *sp;
-    __syncthreads();  // every thread has read the scale before it is written
-    if (s_old >= s || s_old != s_old) {
-      s = s_old;  // NaN stays NaN
-    } else if (s != s_old) {
-      // the older rows of the block under the larger (or NaN) scale
-      for (int i = threadIdx.x; i < n_old * a.dh / 4; i += kAppendThreads) {
-        uint32_t w = reinterpret_cast<uint32_t*>(dst)[i], r = 0;
-        if (s == s) {
+    for (int w = 1; w < NT / 32; ++w) mx = max(mx, red[w0 + w]);
+  }
+  uint8_t* dst = (is_v ? a.v_ctx : a.k_ctx) + ((long long)(b * a.Hkv + g) * a.L_cap + p0) * a.dh;
+  float* sp = (is_v ? a.v_scale : a.k_scale) + (long long)(b * a.Hkv + g) * a.n_blocks + blk;
+  float s = q8_scale<TYPE>(mx), s_old = s;
+  if (n_old > 0) s_old = *sp;
+  // every thread has read the scale before it is written
+  if constexpr (NT > 32) {
+    if (kCta != NT || n_old > 0) __syncthreads();
+  } else {
+    __syncwarp();
+  }
+  if (!mine) return;
+  if (s_old >= s || s_old != s_old) {
+    s = s_old;  // NaN stays NaN
+  } else if (s != s_old) {
+    // the older rows of the block under the larger (or NaN) scale
+    for (int i = tid; i < n_old * a.dh / 4; i += NT) {
+      uint32_t w = reinterpret_cast<uint32_t*>(dst)[i], r = 0;
+      if (s == s) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) r |= q8_recode<TYPE>((w >> e) & 255u, s_old, s) << e;
-        }
-        reinterpret_cast<uint32_t*>(dst)[i] = r;
+        for (int e = 0; e < 32; e += 8) r |= q8_recode<TYPE>((w >> e) & 255u, s_old, s) << e;
       }
+      reinterpret_cast<uint32_t*>(dst)[i] = r;
     }
   }
   const float inv = 1.f / s;
   const bool ok = s == s;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const int i = lo + k * kAppendThreads + threadIdx.x;
+  for (int k = 0; k < kVec; ++k) {
+    const int i = lo + k * NT + tid;
     if (i < hi)
       *reinterpret_cast<uint2*>(dst + (long long)i * 8) =
           ok ? q8_pack8<TYPE>(x[k], s, inv) : make_uint2(0, 0);
   }
-  if (threadIdx.x == 0) *sp = s;
+  if (tid == 0) *sp = s;
 }
 
-// ctx_len[b] += rows appended, after every block of the sequence is written.
+// After every block is written: ctx_len[b] += rows appended, and the error
+// word (one CTA: it reports for all sequences).
 __global__ void __launch_bounds__(256) append_len_kernel(const AppendQ8Args a) {
   griddep_launch();
   griddep_wait();
-  const int b = blockIdx.x * blockDim.x + threadIdx.x;
-  if (b >= a.B) return;
-  const int L = a.ctx_len[b];
-  const int m = append_rows(a, b, L);
-  if (m > 0) a.ctx_len[b] = L + m;
+  int bad = 0;
+  for (int b = threadIdx.x; b < a.B; b += 256) {
+    const int L = a.ctx_len[b];
+    const int m = append_rows(a, b, L);
+    bad |= m < 0;
+    if (m > 0) a.ctx_len[b] = L + m;
+  }
+  bad = __syncthreads_or(bad);
+  if (threadIdx.x == 0) {
+    a.err[0] = bad ? (int)TT_ERR_INVALID_ARG : 0;
+    a.err[1] = 0;
+  }
 }
 
 // Row r of x (row rowlist[r] of it with a row list) to int8 codes and a
@@ -154,13 +175,30 @@ __global__ void __launch_bounds__(kQuantThreads)
 
 }  // namespace
 
+template <int TYPE, int NT>
+static cudaError_t launch_append(const AppendQ8Args& a, cudaStream_t st) {
+  constexpr int kCta = NT < 128 ? 128 : NT, kPer = kCta / NT;
+  const long long items = ((a.n + a.block - 1) / a.block + 1) * 2ll * a.Hkv * a.B;
+  return launch_k(append_q8_kernel<TYPE, NT>, dim3((unsigned)((items + kPer - 1) / kPer)),
+                  dim3(kCta), 0, st, a);
+}
+template <int TYPE>
+static cudaError_t launch_append_type(const AppendQ8Args& a, cudaStream_t st) {
+  switch (append_block_threads(a.block * a.dh)) {
+    case 32: return launch_append<TYPE, 32>(a, st);
+    case 64: return launch_append<TYPE, 64>(a, st);
+    case 128: return launch_append<TYPE, 128>(a, st);
+    case 256: return launch_append<TYPE, 256>(a, st);
+    default: return launch_append<TYPE, 512>(a, st);
+  }
+}
+
 cudaError_t launch_append_q8(const AppendQ8Args& a, int type, cudaStream_t st) {
-  const dim3 grid((unsigned)(((a.n + a.block - 1) / a.block + 1) * 2ll * a.Hkv * a.B));
-  cudaError_t e = type == TT_Q8_INT8
-                      ? launch_k(append_q8_kernel<TT_Q8_INT8>, grid, dim3(kAppendThreads), 0, st, a)
-                      : launch_k(append_q8_kernel<TT_Q8_E4M3>, grid, dim3(kAppendThreads), 0, st, a);
-  if (e != cudaSuccess) return e;
-  return launch_k(append_len_kernel, dim3((a.B + 255) / 256), dim3(256), 0, st, a);
+  return type == TT_Q8_INT8 ? launch_append_type<TT_Q8_INT8>(a, st)
+                            : launch_append_type<TT_Q8_E4M3>(a, st);
+}
+cudaError_t launch_append_q8_len(const AppendQ8Args& a, cudaStream_t st) {
+  return launch_k(append_len_kernel, dim3(1), dim3(256), 0, st, a);
 }
 
 cudaError_t launch_quant_rows(const uint16_t* x, int K, int8_t* q, float* scale,

@@ -16,6 +16,8 @@ struct AppendQ8Args {
   int* err;
 };
 cudaError_t launch_append_q8(const AppendQ8Args& a, int type, cudaStream_t st);
+// ctx_len and the error word, after launch_append_q8.
+cudaError_t launch_append_q8_len(const AppendQ8Args& a, cudaStream_t st);
 
 // Row r < rows (or < *M_dev) of x, or row rowlist[r] of it: int8 codes q[r, :]
 // and scale[r].

@@ -3,10 +3,11 @@
 // The code of x under scale s is x / s rounded to the nearest code, ties to
 // even, as if the quotient were exact.  The quotient is taken as x * (1 / s):
 // two roundings, at most 2^-22.4 relative off.  That decides the nearest code
-// unless it lies next to the middle of two codes; there (about one value in
-// a thousand) the sign of x - h s decides, h being the middle: a product of
-// a short and a 24-bit significand less x, so one FMA rounds it without
-// losing the sign, and 0 is a true tie.
+// unless it lies next to the middle of two codes; there (a value in some
+// thousands) the sign of x - h s decides, h being the middle: a product of a
+// short and a 24-bit significand less x, so one FMA rounds it without losing
+// the sign, and 0 is a true tie.  Eight values share one test for it: about
+// seven instructions a value, which keeps the writers bound by HBM.
 #pragma once
 #include <stdint.h>
 
@@ -38,56 +39,81 @@ __device__ __forceinline__ float round_exact(float y, float s, float t, float st
   return (r > 0.f ? lo + 1.f : r < 0.f ? lo : even) * step;
 }
 
-// int8 code of x (|x| <= 127 s up to the rounding of s), inv = 1 / s.
-__device__ __forceinline__ int q8_int8(float x, float s, float inv) {
-  const float t = x * inv;
-  float n = rintf(t);
-  // |t| <= 127.0001 and its error is below 127 * 2^-22 < 2^-15
-  if (fabsf(t - n) > 0.49996f) n = copysignf(round_exact(fabsf(x), s, fabsf(t), 1.f), x);
-  return (int)fminf(fmaxf(n, -127.f), 127.f);
-}
-
 __device__ __forceinline__ uint32_t cvt_e4m3x2(float lo, float hi) {
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
   return r;
 }
-
-// The e4m3 value nearest to x / s as a float: exact near the middle of two
-// codes (the 20 bits below a normal's third mantissa bit near 0x80000) and
-// for the subnormal codes, whose spacing is 2^-9; x / s itself elsewhere (the
-// conversion rounds it).
-__device__ __forceinline__ float e4m3_near(float x, float s, float inv) {
-  const float t = x * inv;
-  const uint32_t u = __float_as_uint(t) & 0x7FFFFFFFu;
-  const uint32_t d = (u & 0xFFFFFu) - (0x80000u - 16u);
-  if (d > 32u && u >= 0x3C800000u) return t;  // 0x3C800000: 2^-6
-  if (u == 0u) return t;
-  const int e = max((int)(u >> 23) - 127, -6);
-  const float step = __uint_as_float((uint32_t)(e - 3 + 127) << 23);
-  return copysignf(round_exact(fabsf(x), s, fabsf(t), step), x);
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
+  return __byte_perm(a, b, sel);
 }
 
-// Four codes as bytes, lowest first.
+// The exact code of one value as a byte.
 template <int TYPE>
-__device__ __forceinline__ uint32_t q8_pack4(float a, float b, float c, float d, float s,
-                                             float inv) {
+__device__ __forceinline__ uint32_t q8_exact(float x, float s, float t) {
   if constexpr (TYPE == TT_Q8_INT8) {
-    return (uint32_t)(q8_int8(a, s, inv) & 255) | (uint32_t)(q8_int8(b, s, inv) & 255) << 8 |
-           (uint32_t)(q8_int8(c, s, inv) & 255) << 16 | (uint32_t)(q8_int8(d, s, inv) & 255) << 24;
+    const float n = round_exact(fabsf(x), s, fabsf(t), 1.f);
+    return (uint32_t)(int)copysignf(fminf(n, 127.f), x) & 255u;
   } else {
-    return cvt_e4m3x2(e4m3_near(a, s, inv), e4m3_near(b, s, inv)) |
-           cvt_e4m3x2(e4m3_near(c, s, inv), e4m3_near(d, s, inv)) << 16;
+    // codes are 2^(e - 3) apart, e the quotient's exponent, at least -6
+    const uint32_t u = __float_as_uint(t) & 0x7FFFFFFFu;
+    const int e = max((int)(u >> 23) - 127, -6);
+    const float step = __uint_as_float((uint32_t)(e - 3 + 127) << 23);
+    return cvt_e4m3x2(copysignf(round_exact(fabsf(x), s, fabsf(t), step), x), 0.f) & 255u;
   }
 }
 
-// Eight bf16 values (one 16-byte vector) to eight codes.
+// Eight bf16 values (one 16-byte vector) to eight codes; inv = 1 / s.
 template <int TYPE>
 __device__ __forceinline__ uint2 q8_pack8(const uint4& v, float s, float inv) {
-  auto lo = [](uint32_t w) { return __uint_as_float(w << 16); };
-  auto hi = [](uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); };
-  return make_uint2(q8_pack4<TYPE>(lo(v.x), hi(v.x), lo(v.y), hi(v.y), s, inv),
-                    q8_pack4<TYPE>(lo(v.z), hi(v.z), lo(v.w), hi(v.w), s, inv));
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  float t[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    t[2 * i] = __uint_as_float(w[i] << 16) * inv;
+    t[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u) * inv;
+  }
+  uint2 r;
+  bool near;
+  if constexpr (TYPE == TT_Q8_INT8) {
+    // adding 1.5 * 2^23 rounds to the nearest integer, whose two's complement
+    // is then in the low byte; |t| < 127.5, and its error is below 2^-15
+    float far = 0.f;
+    uint32_t m[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float k = t[i] + 12582912.f;
+      m[i] = __float_as_uint(k);
+      far = fmaxf(far, fabsf(t[i] - (k - 12582912.f)));
+    }
+    near = far > 0.49996f;
+    r = make_uint2(prmt(prmt(m[0], m[1], 0x40), prmt(m[2], m[3], 0x40), 0x5410),
+                   prmt(prmt(m[4], m[5], 0x40), prmt(m[6], m[7], 0x40), 0x5410));
+  } else {
+    // near a middle: the 20 bits below a normal's third fraction bit near
+    // 0x80000; and all subnormal codes (below 2^-6)
+    uint32_t d = 0xFFFFFFFFu;
+    float low = 1.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      d = min(d, (__float_as_uint(t[i]) & 0xFFFFFu) - (0x80000u - 16u));
+      low = fminf(low, fabsf(t[i]));
+    }
+    near = d <= 32u || low < 0.015625f;
+    r = make_uint2(cvt_e4m3x2(t[0], t[1]) | cvt_e4m3x2(t[2], t[3]) << 16,
+                   cvt_e4m3x2(t[4], t[5]) | cvt_e4m3x2(t[6], t[7]) << 16);
+  }
+  if (near) {
+#pragma unroll 1
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t wi = i < 2 ? v.x : i < 4 ? v.y : i < 6 ? v.z : v.w;
+      const float x = __uint_as_float(i & 1 ? wi & 0xFFFF0000u : wi << 16);
+      const uint32_t b = q8_exact<TYPE>(x, s, x * inv);
+      uint32_t& dst = i < 4 ? r.x : r.y;
+      dst = (dst & ~(255u << (8 * (i & 3)))) | b << (8 * (i & 3));
+    }
+  }
+  return r;
 }
 
 // Largest magnitude of eight bf16 values, merged into two running 16-bit
