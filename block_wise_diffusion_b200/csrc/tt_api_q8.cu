@@ -50,6 +50,8 @@ tt_status check_fmt(const tt_q8* f) {
   return TT_OK;
 }
 
+int block_shift(const tt_q8& f) { return f.block == 16 ? 4 : f.block == 32 ? 5 : f.block == 64 ? 6 : 7; }
+
 tt_status check_ws_ptr(void* ws, size_t have, size_t need) {
   Q8_CHECK(check_ptr(ws, "ws", 256));
   if (have < need)
@@ -205,7 +207,7 @@ tt_status tt_block_denoise_attn_q8(const tt_dims* d, const tt_q8* f, const tt_bf
   a.dh = d->dh;
   a.G = d->Hq / d->Hkv;
   a.L_cap = d->L_cap;
-  a.block_shift = f->block == 16 ? 4 : f->block == 32 ? 5 : f->block == 64 ? 6 : 7;
+  a.block_shift = block_shift(*f);
   a.n_blocks = (d->L_cap + f->block - 1) / f->block;
   a.q = q_blk;
   a.k_blk = k_blk;
@@ -258,7 +260,7 @@ tt_status tt_append_ctx_q8(const tt_dims* d, const tt_q8* f, int32_t n, const in
   Q8_CHECK(check_ptr(v_scale, "v_scale", 4));
   Q8_CHECK(check_ptr(ctx_len, "ctx_len", 4));
   Q8_CHECK(check_ws_ptr(ws, ws_bytes, q8_workspace_bytes(*d, TT_WS_APPEND_Q8)));
-  if (((n + f->block - 1ll) / f->block + 1) * 2 * d->Hkv * d->B >= (1ll << 31))
+  if (2ll * d->Hkv * d->B >= (1ll << 31))
     return set_errorf(TT_ERR_UNSUPPORTED, "problem too large");
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   AppendQ8Args a{};
@@ -267,7 +269,7 @@ tt_status tt_append_ctx_q8(const tt_dims* d, const tt_q8* f, int32_t n, const in
   a.dh = d->dh;
   a.L_cap = d->L_cap;
   a.n = n;
-  a.block = f->block;
+  a.block_shift = block_shift(*f);
   a.n_blocks = (d->L_cap + f->block - 1) / f->block;
   a.new_len = new_len;
   a.k_new = k_new;

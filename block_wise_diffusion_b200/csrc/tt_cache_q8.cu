@@ -2,6 +2,8 @@
 // quantised one by one for the integer products.  Both read each bf16 value
 // once (a group stays in registers between its maximum and its rounding) and
 // are bound by HBM: 2 bytes in and 1 byte out per value.
+#include <algorithm>
+
 #include "tt_q8.h"
 #include "tt_quant.cuh"
 
@@ -9,11 +11,11 @@ namespace tt {
 
 namespace {
 
-// A thread holds kVec vectors of 8 values of one cache block, so a block of
-// block * dh values takes block * dh / 32 threads: 32 (16 x 64) to 512 (128 x
-// 128).  A CTA has at least 128 threads, several blocks where they are small.
-constexpr int kVec = 4;
-constexpr int append_block_threads(int block_values) { return block_values / (8 * kVec); }
+// A thread holds KV vectors of 8 values of one cache block, 8 of them except
+// in the smallest blocks, so a block of block * dh values takes 32 (16 x 64) to
+// 256 (128 x 128) threads.  A CTA has at least 128 threads, several blocks
+// side by side where they are small.
+constexpr int append_vectors(int block_values) { return block_values >= 2048 ? 8 : 4; }
 
 // How many rows sequence b gets, or -1 when its lengths are out of range.
 __device__ __forceinline__ int append_rows(const AppendQ8Args& a, int b, int L) {
@@ -21,90 +23,86 @@ __device__ __forceinline__ int append_rows(const AppendQ8Args& a, int b, int L) 
   return (m < 0 || m > a.n || L < 0 || L > a.L_cap - m) ? -1 : m;
 }
 
-// Item (b, g, K or V, i), i fastest: the i-th cache block that sequence b's new
-// rows may touch, counted from the block that holds its end.  NT: threads of a
-// block.
-template <int TYPE, int NT>
+// CTA (x, y): of the pairs (b, g, K or V) y, y + gridDim.y, .., the x-th group
+// of cache blocks that sequence b's new rows may touch, counted from the block
+// that holds its end.  NT: threads of a block.
+template <int TYPE, int NT, int KV>
 __global__ void __launch_bounds__(NT < 128 ? 128 : NT) append_q8_kernel(const AppendQ8Args a) {
   constexpr int kCta = NT < 128 ? 128 : NT;
   griddep_launch();
   griddep_wait();
   __shared__ uint32_t red[kCta / 32];
-  const int nb = (a.n + a.block - 1) / a.block + 1;
-  const int tid = threadIdx.x % NT;
-  const unsigned item = blockIdx.x * (kCta / NT) + threadIdx.x / NT;
-  const int pair = (int)(item / nb), bi = (int)(item - (unsigned)pair * nb);
-  const int is_v = pair & 1, b = (pair >> 1) / a.Hkv, g = (pair >> 1) - b * a.Hkv;
-  int L = 0, m = 0;
-  if (b < a.B) {
-    L = a.ctx_len[b];
-    m = append_rows(a, b, L);
-  }
-  const int blk = L / a.block + bi;
-  const long long p0 = (long long)blk * a.block;  // first position of the block
-  const bool mine = m > 0 && p0 < (long long)L + m;
-  if (kCta == NT && !mine) return;
-  const int n_old = mine ? max(0, (int)(L - p0)) : 0;  // older rows in the block
-  const int n_end = mine ? (int)min((long long)a.block, L + m - p0) : 0;
-  const int dv_log = a.dh == 64 ? 3 : 4;              // vectors per row: 8 or 16
-  const int lo = n_old << dv_log, hi = n_end << dv_log;  // new vectors of the block
-  const uint16_t* src = (is_v ? a.v_new : a.k_new) + (long long)b * a.stride_b +
-                        (long long)g * a.stride_h + (p0 - L) * a.stride_t;
-  uint4 x[kVec];
-  uint32_t mx = 0;
+  const int tid = threadIdx.x % NT, bi = blockIdx.x * (kCta / NT) + threadIdx.x / NT;
+  const int pairs = 2 * a.Hkv * a.B;
+  for (int pair = blockIdx.y; pair < pairs; pair += gridDim.y) {
+    const int is_v = pair & 1, b = (pair >> 1) / a.Hkv, g = (pair >> 1) - b * a.Hkv;
+    const int L = a.ctx_len[b], m = append_rows(a, b, L);
+    const int blk = (max(L, 0) >> a.block_shift) + bi;
+    const long long p0 = (long long)blk << a.block_shift;  // first position of the block
+    const bool mine = m > 0 && p0 < (long long)L + m;
+    if (kCta == NT && !mine) continue;
+    const int n_old = mine ? max(0, (int)(L - p0)) : 0;  // older rows in the block
+    const int n_end = mine ? (int)min(1ll << a.block_shift, L + m - p0) : 0;
+    const int dv_log = a.dh == 64 ? 3 : 4;              // vectors per row: 8 or 16
+    const int lo = n_old << dv_log, hi = n_end << dv_log;  // new vectors of the block
+    const uint16_t* src = (is_v ? a.v_new : a.k_new) + (long long)b * a.stride_b +
+                          (long long)g * a.stride_h + (p0 - L) * a.stride_t;
+    uint4 x[KV];
+    uint32_t mx = 0;
 #pragma unroll
-  for (int k = 0; k < kVec; ++k) {
-    const int i = lo + k * NT + tid;
-    if (i < hi) {
-      const int t = i >> dv_log;
-      x[k] = *reinterpret_cast<const uint4*>(src + (long long)t * a.stride_t +
-                                             (i - (t << dv_log)) * 8);
-      mx = absmax8(mx, x[k]);
-    }
-  }
-  mx = __reduce_max_sync(0xffffffffu, absmax_fold(mx));
-  if constexpr (NT > 32) {
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = mx;
-    __syncthreads();
-    const int w0 = threadIdx.x / NT * (NT / 32);
-    mx = red[w0];
-#pragma unroll
-    for (int w = 1; w < NT / 32; ++w) mx = max(mx, red[w0 + w]);
-  }
-  uint8_t* dst = (is_v ? a.v_ctx : a.k_ctx) + ((long long)(b * a.Hkv + g) * a.L_cap + p0) * a.dh;
-  float* sp = (is_v ? a.v_scale : a.k_scale) + (long long)(b * a.Hkv + g) * a.n_blocks + blk;
-  float s = q8_scale<TYPE>(mx), s_old = s;
-  if (n_old > 0) s_old = *sp;
-  // every thread has read the scale before it is written
-  if constexpr (NT > 32) {
-    if (kCta != NT || n_old > 0) __syncthreads();
-  } else {
-    __syncwarp();
-  }
-  if (!mine) return;
-  if (s_old >= s || s_old != s_old) {
-    s = s_old;  // NaN stays NaN
-  } else if (s != s_old) {
-    // the older rows of the block under the larger (or NaN) scale
-    for (int i = tid; i < n_old * a.dh / 4; i += NT) {
-      uint32_t w = reinterpret_cast<uint32_t*>(dst)[i], r = 0;
-      if (s == s) {
-#pragma unroll
-        for (int e = 0; e < 32; e += 8) r |= q8_recode<TYPE>((w >> e) & 255u, s_old, s) << e;
+    for (int k = 0; k < KV; ++k) {
+      const int i = lo + k * NT + tid;
+      if (i < hi) {
+        const int t = i >> dv_log;
+        x[k] = *reinterpret_cast<const uint4*>(src + (long long)t * a.stride_t +
+                                               (i - (t << dv_log)) * 8);
+        mx = absmax8(mx, x[k]);
       }
-      reinterpret_cast<uint32_t*>(dst)[i] = r;
     }
-  }
-  const float inv = 1.f / s;
-  const bool ok = s == s;
+    mx = __reduce_max_sync(0xffffffffu, absmax_fold(mx));
+    if constexpr (NT > 32) {
+      if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = mx;
+      __syncthreads();
+      const int w0 = threadIdx.x / NT * (NT / 32);
+      mx = red[w0];
 #pragma unroll
-  for (int k = 0; k < kVec; ++k) {
-    const int i = lo + k * NT + tid;
-    if (i < hi)
-      *reinterpret_cast<uint2*>(dst + (long long)i * 8) =
-          ok ? q8_pack8<TYPE>(x[k], s, inv) : make_uint2(0, 0);
+      for (int w = 1; w < NT / 32; ++w) mx = max(mx, red[w0 + w]);
+    }
+    uint8_t* dst = (is_v ? a.v_ctx : a.k_ctx) + ((long long)(b * a.Hkv + g) * a.L_cap + p0) * a.dh;
+    float* sp = (is_v ? a.v_scale : a.k_scale) + (long long)(b * a.Hkv + g) * a.n_blocks + blk;
+    float s = q8_scale<TYPE>(mx), s_old = s;
+    if (n_old > 0) s_old = *sp;
+    // every thread has read the scale before it is written, and `red` before the
+    // next pair
+    if constexpr (NT > 32)
+      __syncthreads();
+    else
+      __syncwarp();
+    if (!mine) continue;
+    if (s_old >= s || s_old != s_old) {
+      s = s_old;  // NaN stays NaN
+    } else if (s != s_old) {
+      // the older rows of the block under the larger (or NaN) scale
+      for (int i = tid; i < n_old * a.dh / 4; i += NT) {
+        uint32_t w = reinterpret_cast<uint32_t*>(dst)[i], r = 0;
+        if (s == s) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) r |= q8_recode<TYPE>((w >> e) & 255u, s_old, s) << e;
+        }
+        reinterpret_cast<uint32_t*>(dst)[i] = r;
+      }
+    }
+    const float inv = 1.f / s;
+    const bool ok = s == s;
+#pragma unroll
+    for (int k = 0; k < KV; ++k) {
+      const int i = lo + k * NT + tid;
+      if (i < hi)
+        *reinterpret_cast<uint2*>(dst + (long long)i * 8) =
+            ok ? q8_pack8<TYPE>(x[k], s, inv) : make_uint2(0, 0);
+    }
+    if (tid == 0) *sp = s;
   }
-  if (tid == 0) *sp = s;
 }
 
 // After every block is written: ctx_len[b] += rows appended, and the error
@@ -175,21 +173,21 @@ __global__ void __launch_bounds__(kQuantThreads)
 
 }  // namespace
 
-template <int TYPE, int NT>
+template <int TYPE, int NT, int KV>
 static cudaError_t launch_append(const AppendQ8Args& a, cudaStream_t st) {
   constexpr int kCta = NT < 128 ? 128 : NT, kPer = kCta / NT;
-  const long long items = ((a.n + a.block - 1) / a.block + 1) * 2ll * a.Hkv * a.B;
-  return launch_k(append_q8_kernel<TYPE, NT>, dim3((unsigned)((items + kPer - 1) / kPer)),
-                  dim3(kCta), 0, st, a);
+  const int nb = ((a.n - 1) >> a.block_shift) + 2;  // blocks n rows may touch
+  const dim3 grid((nb + kPer - 1) / kPer, (unsigned)std::min(2 * a.Hkv * a.B, 65535));
+  return launch_k(append_q8_kernel<TYPE, NT, KV>, grid, dim3(kCta), 0, st, a);
 }
 template <int TYPE>
 static cudaError_t launch_append_type(const AppendQ8Args& a, cudaStream_t st) {
-  switch (append_block_threads(a.block * a.dh)) {
-    case 32: return launch_append<TYPE, 32>(a, st);
-    case 64: return launch_append<TYPE, 64>(a, st);
-    case 128: return launch_append<TYPE, 128>(a, st);
-    case 256: return launch_append<TYPE, 256>(a, st);
-    default: return launch_append<TYPE, 512>(a, st);
+  const int values = a.dh << a.block_shift, kv = append_vectors(values);
+  switch (values / (8 * kv)) {
+    case 32: return kv == 4 ? launch_append<TYPE, 32, 4>(a, st) : launch_append<TYPE, 32, 8>(a, st);
+    case 64: return launch_append<TYPE, 64, 8>(a, st);
+    case 128: return launch_append<TYPE, 128, 8>(a, st);
+    default: return launch_append<TYPE, 256, 8>(a, st);
   }
 }
 

@@ -6,7 +6,8 @@ namespace tt {
 
 // ------------------------------------------------------------ cache append
 struct AppendQ8Args {
-  int B, Hkv, dh, L_cap, n, block, n_blocks;  // n_blocks: scales per (sequence, head)
+  int B, Hkv, dh, L_cap, n, n_blocks;  // n_blocks: scales per (sequence, head)
+  int block_shift;                     // 2^block_shift positions per scale
   const int* new_len;                         // optional [B]
   const uint16_t *k_new, *v_new;
   long long stride_b, stride_t, stride_h;     // elements

@@ -1,13 +1,15 @@
 // Rounding to 8-bit codes with a scale, shared by the kernels that write them.
 //
 // The code of x under scale s is x / s rounded to the nearest code, ties to
-// even, as if the quotient were exact.  The quotient is taken as x * (1 / s):
-// two roundings, at most 2^-22.4 relative off.  That decides the nearest code
-// unless it lies next to the middle of two codes; there (a value in some
-// thousands) the sign of x - h s decides, h being the middle: a product of a
-// short and a 24-bit significand less x, so one FMA rounds it without losing
-// the sign, and 0 is a true tie.  Eight values share one test for it: about
-// seven instructions a value, which keeps the writers bound by HBM.
+// even, as if the quotient were exact.  The quotient is taken as t = x * (1 /
+// s): two roundings, at most two units of its last place off.  t gives the two
+// codes around x / s and the middle h between them (next to a code itself it
+// may give the wrong pair, but then the same nearest code), and the sign of
+// x - h s decides: h has a short significand, so one FMA rounds that
+// difference without losing its sign, and 0 is a true tie.
+// Such quotients are no rarity: half a group's largest value always lies within
+// a rounding of a middle of int8 codes (63.5), one value in a thousand of
+// normal data.  So nothing here takes a long path for them.
 #pragma once
 #include <stdint.h>
 
@@ -74,36 +76,59 @@ __device__ __forceinline__ uint2 q8_pack8(const uint4& v, float s, float inv) {
     t[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u) * inv;
   }
   uint2 r;
-  bool near;
+  bool rare;
   if constexpr (TYPE == TT_Q8_INT8) {
-    // adding 1.5 * 2^23 rounds to the nearest integer, whose two's complement
-    // is then in the low byte; |t| < 127.5, and its error is below 2^-15
-    float far = 0.f;
+    // Rounded down by adding 1.5 * 2^23 (the integer's two's complement is then
+    // in the low byte), and up by one where x lies above the middle.
     uint32_t m[8];
+    float tie = 1.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float k = t[i] + 12582912.f;
-      m[i] = __float_as_uint(k);
-      far = fmaxf(far, fabsf(t[i] - (k - 12582912.f)));
+      const float x = __uint_as_float(i & 1 ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16);
+      const float k = __fadd_rd(t[i], 12582912.f);
+      const float d = fmaf(-((k - 12582912.f) + 0.5f), s, x);
+      m[i] = __float_as_uint(k) + 1u + (uint32_t)(__float_as_int(d) >> 31);
+      tie = fminf(tie, fabsf(d));
     }
-    near = far > 0.49996f;
+    rare = tie == 0.f;
     r = make_uint2(prmt(prmt(m[0], m[1], 0x40), prmt(m[2], m[3], 0x40), 0x5410),
                    prmt(prmt(m[4], m[5], 0x40), prmt(m[6], m[7], 0x40), 0x5410));
   } else {
-    // near a middle: the 20 bits below a normal's third fraction bit near
-    // 0x80000; and all subnormal codes (below 2^-6)
+    // The conversion rounds t; that may be wrong only with the 20 bits below a
+    // normal's third fraction bit within 4 of 0x80000, or below 2^-6, where
+    // codes are 2^-9 apart.  Then the codes around t by its upper bits (below
+    // 2^-6: of t + 2^-6, whose spacing is theirs), up by one above the middle.
     uint32_t d = 0xFFFFFFFFu;
     float low = 1.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      d = min(d, (__float_as_uint(t[i]) & 0xFFFFFu) - (0x80000u - 16u));
+      d = min(d, (__float_as_uint(t[i]) & 0xFFFFFu) - (0x80000u - 4u));
       low = fminf(low, fabsf(t[i]));
     }
-    near = d <= 32u || low < 0.015625f;
     r = make_uint2(cvt_e4m3x2(t[0], t[1]) | cvt_e4m3x2(t[2], t[3]) << 16,
                    cvt_e4m3x2(t[4], t[5]) | cvt_e4m3x2(t[6], t[7]) << 16);
+    rare = false;
+    if (d <= 8u || low < 0.015625f) {
+      uint32_t c[8];
+      float tie = 1.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t xb = i & 1 ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16;
+        const bool sub = fabsf(t[i]) < 0.015625f;
+        const float o = sub ? 0.015625f : 0.f;
+        const uint32_t y = __float_as_uint(fabsf(t[i]) + o);
+        const float h = __uint_as_float((y & 0xFFF00000u) | 0x80000u) - o;
+        const float e = fmaf(-h, s, __uint_as_float(xb & 0x7FFFFFFFu));
+        c[i] = ((y >> 20) - (sub ? 968u : 960u) + 1u + (uint32_t)(__float_as_int(e) >> 31)) |
+               (xb >> 24 & 0x80u);
+        tie = fminf(tie, fabsf(e));
+      }
+      rare = tie == 0.f;
+      r = make_uint2(prmt(prmt(c[0], c[1], 0x40), prmt(c[2], c[3], 0x40), 0x5410),
+                     prmt(prmt(c[4], c[5], 0x40), prmt(c[6], c[7], 0x40), 0x5410));
+    }
   }
-  if (near) {
+  if (rare) {  // a true tie: to even
 #pragma unroll 1
     for (int i = 0; i < 8; ++i) {
       const uint32_t wi = i < 2 ? v.x : i < 4 ? v.y : i < 6 ? v.z : v.w;
