@@ -420,22 +420,41 @@ def q8(kind: str, block: int) -> Q8:
     return Q8({"int8": TT_Q8_INT8, "e4m3": TT_Q8_E4M3}[kind], int(block))
 
 
-def _one_device(*tensors) -> None:
-    """Refuses tensors that are not on the current device: the kernels are
-    launched there, on its current stream unless another is given."""
-    import torch
-    cur = None
-    for t in tensors:
-        if t is None or isinstance(t, int) or not t.is_cuda:
-            continue
-        if cur is None:
-            cur = torch.cuda.current_device()
-        if t.get_device() != cur:
-            raise ValueError(f"tensor on cuda:{t.get_device()}, current device is cuda:{cur}")
+_torch = None
 
 
-def _n_scales(d: Dims, f: Q8) -> int:
-    return d.B * d.Hkv * -(-d.L_cap // max(f.block, 1))
+def _device() -> int:
+    """The current device: these calls launch there, on its current stream
+    unless another is given, so every tensor has to live there."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch.cuda.current_device() if _torch.cuda.is_initialized() else -1
+
+
+def _arg(x, name: str, nbytes: int, dev: int) -> int | None:
+    """Address of a tensor argument after the checks of _sized and of its
+    device, with as few tensor calls as they take: a small call's time is the
+    host's.  Raw integer addresses carry no size and pass unchecked."""
+    if x is None or type(x) is int:
+        return x
+    if x.nbytes < nbytes:
+        raise ValueError(f"{name} holds {x.nbytes} bytes; these dims need {nbytes}")
+    at = x.get_device()
+    if at < 0:
+        raise ValueError("libtwotower takes CUDA tensors only (no CPU path)")
+    if not x.is_contiguous():
+        raise ValueError("tensor must be contiguous")
+    if at != dev:
+        raise ValueError(f"{name} is on cuda:{at}, the current device is cuda:{dev}")
+    return x.data_ptr()
+
+
+def _raw_stream(stream, dev: int) -> int | None:
+    if stream is None:
+        return _torch._C._cuda_getCurrentRawStream(dev)
+    return stream if type(stream) is int else stream.cuda_stream
 
 
 def tt_block_denoise_attn_q8(d: Dims, f: Q8, q_blk, k_blk, v_blk, k_ctx, v_ctx, k_scale, v_scale,
@@ -443,27 +462,32 @@ def tt_block_denoise_attn_q8(d: Dims, f: Q8, q_blk, k_blk, v_blk, k_ctx, v_ctx, 
     """tt_block_denoise_attn over a context cache held in 8 bits: codes
     [B, Hkv, L_cap, dh] (int8 or float8_e4m3fn) and one float32 scale per
     `f.block` positions and KV head."""
-    rows, ctx, ns = d.B * d.S, d.B * d.Hkv * d.L_cap * d.dh, _n_scales(d, f) * 4
-    _one_device(q_blk, k_blk, v_blk, k_ctx, v_ctx, k_scale, v_scale, ctx_len, out, ws)
-    _check(lib().tt_block_denoise_attn_q8(
-        ctypes.byref(d), ctypes.byref(f), _sized(q_blk, "q_blk", rows * d.Hq * d.dh * 2),
-        _sized(k_blk, "k_blk", rows * d.Hkv * d.dh * 2),
-        _sized(v_blk, "v_blk", rows * d.Hkv * d.dh * 2), _sized(k_ctx, "k_ctx", ctx),
-        _sized(v_ctx, "v_ctx", ctx), _sized(k_scale, "k_scale", ns),
-        _sized(v_scale, "v_scale", ns), _sized(ctx_len, "ctx_len", d.B * 4),
-        _sized(out, "out", rows * d.Hq * d.dh * 2), _ptr(ws), _nbytes(ws), _stream(stream)),
-        "tt_block_denoise_attn_q8")
+    B, S, Hq, Hkv, dh, L_cap, block = d.B, d.S, d.Hq, d.Hkv, d.dh, d.L_cap, f.block
+    q, kv, ctx = 2 * B * S * Hq * dh, 2 * B * S * Hkv * dh, B * Hkv * L_cap * dh
+    ns = 4 * B * Hkv * -(-L_cap // block) if block > 0 else 0
+    dev = _device()
+    code = lib().tt_block_denoise_attn_q8(
+        d, f, _arg(q_blk, "q_blk", q, dev), _arg(k_blk, "k_blk", kv, dev),
+        _arg(v_blk, "v_blk", kv, dev), _arg(k_ctx, "k_ctx", ctx, dev),
+        _arg(v_ctx, "v_ctx", ctx, dev), _arg(k_scale, "k_scale", ns, dev),
+        _arg(v_scale, "v_scale", ns, dev), _arg(ctx_len, "ctx_len", 4 * B, dev),
+        _arg(out, "out", q, dev), _arg(ws, "ws", 0, dev), _nbytes(ws), _raw_stream(stream, dev))
+    if code:
+        _check(code, "tt_block_denoise_attn_q8")
 
 
-def _rows_arg(x, name: str, d: Dims, n: int) -> int:
-    """Address of a strided [B, n, Hkv, dh] bf16 tensor with a dense last dimension."""
-    if not x.is_cuda:
+def _rows_arg(x, name: str, shape: tuple, dev: int) -> tuple[int, tuple]:
+    """Address and strides of a [B, n, Hkv, dh] bf16 tensor with a dense last
+    dimension; a dimension of one element has no stride of its own (0)."""
+    at, st = x.get_device(), x.stride()
+    if at < 0:
         raise ValueError("libtwotower takes CUDA tensors only (no CPU path)")
-    if tuple(x.shape) != (d.B, n, d.Hkv, d.dh) or x.element_size() != 2 or \
-            (x.stride(3) != 1 and d.dh > 1):
-        raise ValueError(f"{name} must be a 16-bit tensor of shape {(d.B, n, d.Hkv, d.dh)} with a "
-                         f"dense last dimension; got {tuple(x.shape)}, strides {x.stride()}")
-    return x.data_ptr()
+    if x.shape != shape or x.element_size() != 2 or st[3] != 1:
+        raise ValueError(f"{name} must be a 16-bit tensor of shape {shape} with a dense last "
+                         f"dimension; got {tuple(x.shape)}, strides {st}")
+    if at != dev:
+        raise ValueError(f"{name} is on cuda:{at}, the current device is cuda:{dev}")
+    return x.data_ptr(), tuple(0 if k == 1 else a for k, a in zip(shape[:3], st))
 
 
 def tt_append_ctx_q8(d: Dims, f: Q8, n: int, new_len, k_new, v_new, k_ctx, v_ctx, k_scale, v_scale,
@@ -472,29 +496,32 @@ def tt_append_ctx_q8(d: Dims, f: Q8, n: int, new_len, k_new, v_new, k_ctx, v_ctx
     k_new / v_new [B, n, Hkv, dh] onto the end of each sequence's 8-bit cache;
     ctx_len grows in place.  k_new and v_new may be strided views (the last
     dimension dense, both with the same strides)."""
-    ctx, ns = d.B * d.Hkv * d.L_cap * d.dh, _n_scales(d, f) * 4
-    k_ptr, v_ptr = _rows_arg(k_new, "k_new", d, n), _rows_arg(v_new, "v_new", d, n)
-    sk, sv = k_new.stride(), v_new.stride()
-    # a dimension of one element has no stride of its own
-    st = [0 if size == 1 else a for size, a in zip(k_new.shape, sk)][:3]
-    if st != [0 if size == 1 else a for size, a in zip(v_new.shape, sv)][:3]:
-        raise ValueError(f"k_new and v_new need the same strides; got {sk} and {sv}")
-    _one_device(new_len, k_new, v_new, k_ctx, v_ctx, k_scale, v_scale, ctx_len, ws)
-    _check(lib().tt_append_ctx_q8(
-        ctypes.byref(d), ctypes.byref(f), int(n), _sized(new_len, "new_len", d.B * 4), k_ptr, v_ptr,
-        ctypes.byref(_RowStrides(*st)), _sized(k_ctx, "k_ctx", ctx), _sized(v_ctx, "v_ctx", ctx),
-        _sized(k_scale, "k_scale", ns), _sized(v_scale, "v_scale", ns),
-        _sized(ctx_len, "ctx_len", d.B * 4), _ptr(ws), _nbytes(ws), _stream(stream)),
-        "tt_append_ctx_q8")
+    B, Hkv, dh, L_cap, block = d.B, d.Hkv, d.dh, d.L_cap, f.block
+    ctx, ns = B * Hkv * L_cap * dh, 4 * B * Hkv * -(-L_cap // block) if block > 0 else 0
+    dev, shape = _device(), (B, n, Hkv, dh)
+    k_ptr, st = _rows_arg(k_new, "k_new", shape, dev)
+    v_ptr, sv = _rows_arg(v_new, "v_new", shape, dev)
+    if st != sv:
+        raise ValueError(f"k_new and v_new need the same strides; got {st} and {sv}")
+    code = lib().tt_append_ctx_q8(
+        d, f, n, _arg(new_len, "new_len", 4 * B, dev), k_ptr, v_ptr, _RowStrides(*st),
+        _arg(k_ctx, "k_ctx", ctx, dev), _arg(v_ctx, "v_ctx", ctx, dev),
+        _arg(k_scale, "k_scale", ns, dev), _arg(v_scale, "v_scale", ns, dev),
+        _arg(ctx_len, "ctx_len", 4 * B, dev), _arg(ws, "ws", 0, dev), _nbytes(ws),
+        _raw_stream(stream, dev))
+    if code:
+        _check(code, "tt_append_ctx_q8")
 
 
 def tt_quantize_rows_i8(rows: int, K: int, x, q, scale, stream=None) -> None:
     """int8 codes q [rows, K] and float32 scales [rows] of bf16 x [rows, K]
     (weights: a row per output channel)."""
-    _one_device(x, q, scale)
-    _check(lib().tt_quantize_rows_i8(
-        int(rows), int(K), _sized(x, "x", rows * K * 2), _sized(q, "q", rows * K),
-        _sized(scale, "scale", rows * 4), _stream(stream)), "tt_quantize_rows_i8")
+    dev = _device()
+    code = lib().tt_quantize_rows_i8(
+        rows, K, _arg(x, "x", 2 * rows * K, dev), _arg(q, "q", rows * K, dev),
+        _arg(scale, "scale", 4 * rows, dev), _raw_stream(stream, dev))
+    if code:
+        _check(code, "tt_quantize_rows_i8")
 
 
 def tt_linear_i8_workspace_bytes(rows: int, N: int, K: int) -> int:
@@ -513,11 +540,13 @@ def linear_i8_workspace(rows: int, N: int, K: int, device="cuda"):
 def tt_linear_i8(rows: int, N: int, K: int, x, w_q, w_scale, out, ws, stream=None) -> None:
     """out [rows, N] = bf16(x [rows, K] . (w_q * w_scale)^T), x quantised per
     row to int8, the sums exact in 32-bit integers."""
-    _one_device(x, w_q, w_scale, out, ws)
-    _check(lib().tt_linear_i8(
-        int(rows), int(N), int(K), _sized(x, "x", rows * K * 2), _sized(w_q, "w_q", N * K),
-        _sized(w_scale, "w_scale", N * 4), _sized(out, "out", rows * N * 2), _ptr(ws), _nbytes(ws),
-        _stream(stream)), "tt_linear_i8")
+    dev = _device()
+    code = lib().tt_linear_i8(
+        rows, N, K, _arg(x, "x", 2 * rows * K, dev), _arg(w_q, "w_q", N * K, dev),
+        _arg(w_scale, "w_scale", 4 * N, dev), _arg(out, "out", 2 * rows * N, dev),
+        _arg(ws, "ws", 0, dev), _nbytes(ws), _raw_stream(stream, dev))
+    if code:
+        _check(code, "tt_linear_i8")
 
 
 def tt_vocab_confidence_commit_i8(d: Dims, y, w_q, w_scale, gamma: float, logit_scale: float,
@@ -525,12 +554,14 @@ def tt_vocab_confidence_commit_i8(d: Dims, y, w_q, w_scale, gamma: float, logit_
                                   stream=None) -> None:
     """tt_vocab_confidence_commit with int8 weights w_q [V, H], one float32
     scale per token, and y quantised per row."""
-    rows = d.B * d.S
-    _one_device(y, w_q, w_scale, tokens, masked, conf_out, argmax_out, n_committed, ws)
-    _check(lib().tt_vocab_confidence_commit_i8(
-        ctypes.byref(d), _sized(y, "y", rows * d.H * 2), _sized(w_q, "w_q", d.V * d.H),
-        _sized(w_scale, "w_scale", d.V * 4), float(gamma), float(logit_scale),
-        _sized(tokens, "tokens", rows * 4), _sized(masked, "masked", rows),
-        _sized(conf_out, "conf_out", rows * 4), _sized(argmax_out, "argmax_out", rows * 4),
-        _sized(n_committed, "n_committed", d.B * 4), _ptr(ws), _nbytes(ws), _stream(stream)),
-        "tt_vocab_confidence_commit_i8")
+    B, H, V = d.B, d.H, d.V
+    rows, dev = B * d.S, _device()
+    code = lib().tt_vocab_confidence_commit_i8(
+        d, _arg(y, "y", 2 * rows * H, dev), _arg(w_q, "w_q", V * H, dev),
+        _arg(w_scale, "w_scale", 4 * V, dev), gamma, logit_scale,
+        _arg(tokens, "tokens", 4 * rows, dev), _arg(masked, "masked", rows, dev),
+        _arg(conf_out, "conf_out", 4 * rows, dev), _arg(argmax_out, "argmax_out", 4 * rows, dev),
+        _arg(n_committed, "n_committed", 4 * B, dev), _arg(ws, "ws", 0, dev), _nbytes(ws),
+        _raw_stream(stream, dev))
+    if code:
+        _check(code, "tt_vocab_confidence_commit_i8")

@@ -295,7 +295,7 @@ tt_status tt_quantize_rows_i8(int32_t rows, int32_t K, const tt_bf16* x, int8_t*
   Q8_CHECK(check_ptr(q, "q", 16));
   Q8_CHECK(check_ptr(scale, "scale", 4));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  Q8_LAUNCH(TT_K_QUANT_I8, st, launch_quant_rows(x, K, q, scale, nullptr, nullptr, rows, st));
+  Q8_LAUNCH(TT_K_QUANT_I8, st, launch_quant_rows(x, K, q, scale, nullptr, nullptr, rows, nullptr, st));
   return TT_OK;
 }
 
@@ -315,9 +315,21 @@ tt_status tt_linear_i8(int32_t rows, int32_t N, int32_t K, const tt_bf16* x, con
   const LinearWs w = carve_linear(rows, K, ws);
   Q8_CHECK(check_ws_ptr(ws, ws_bytes, w.total));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  // Fewer 128-wide tiles than SMs: each is shared by a cluster that splits K
+  // (128 x 4608, K = 4096: 36 tiles of 4 CTAs, @@ us against 22 us on 18 SMs
+  // with 256-wide tiles).  Otherwise 256-wide tiles, one CTA each in turn,
+  // which read A half as often.
+  const long long m_tiles = (rows + kI8BM - 1ll) / kI8BM;
+  const long long tiles128 = m_tiles * ((N + kI8SplitBN - 1ll) / kI8SplitBN);
+  const int sms = num_sms(), nkb = (K + kI8BK - 1) / kI8BK;
+  int splits = 0;
+  if (tiles128 <= sms) {
+    splits = 1;
+    while (splits < kI8MaxSplits && 2 * splits <= nkb && tiles128 * 2 * splits <= sms) splits *= 2;
+  }
   CUtensorMap tmA, tmB;
   if (!make_tmap_2d_u8(&tmA, w.xq, K, rows, K, kI8BK, kI8BM) ||
-      !make_tmap_2d_u8(&tmB, w_q, K, N, K, kI8BK, kI8BN))
+      !make_tmap_2d_u8(&tmB, w_q, K, N, K, kI8BK, splits ? kI8SplitBN : kI8BN))
     return set_errorf(TT_ERR_CUDA, "cuTensorMapEncodeTiled failed for the 8-bit linear update");
   GemmI8Args a{};
   a.M_alloc = rows;
@@ -327,11 +339,15 @@ tt_status tt_linear_i8(int32_t rows, int32_t N, int32_t K, const tt_bf16* x, con
   a.b_scale = w_scale;
   a.C = out;
   a.err = w.ctrl;
-  const long long tiles = ((rows + kI8BM - 1ll) / kI8BM) * ((N + kI8BN - 1ll) / kI8BN);
-  Q8_CUDA(cudaMemsetAsync(w.ctrl, 0, kCtrlBytes, st));
-  Q8_LAUNCH(TT_K_QUANT_I8, st, launch_quant_rows(x, K, w.xq, w.xs, nullptr, nullptr, rows, st));
-  Q8_LAUNCH(TT_K_GEMM_I8, st,
-            launch_gemm_i8_linear(tmA, tmB, a, (int)std::min<long long>(tiles, num_sms()), st));
+  Q8_LAUNCH(TT_K_QUANT_I8, st,
+            launch_quant_rows(x, K, w.xq, w.xs, nullptr, nullptr, rows, w.ctrl, st));
+  if (splits) {
+    Q8_LAUNCH(TT_K_GEMM_I8, st, launch_gemm_i8_split(tmA, tmB, a, splits, st));
+  } else {
+    const long long tiles = m_tiles * ((N + kI8BN - 1ll) / kI8BN);
+    Q8_LAUNCH(TT_K_GEMM_I8, st,
+              launch_gemm_i8_linear(tmA, tmB, a, (int)std::min<long long>(tiles, sms), st));
+  }
   return TT_OK;
 }
 
@@ -355,7 +371,7 @@ tt_status tt_vocab_confidence_commit_i8(const tt_dims* d, const tt_bf16* y, cons
   Q8_CUDA(cudaMemsetAsync(w.ctrl, 0, w.clear, st));
   PlanArgs p{d->B, d->S, masked, w.rowlist, w.tvec, w.ctrl, 0};
   Q8_LAUNCH(TT_K_PLAN, st, launch_plan(p, st));
-  Q8_LAUNCH(TT_K_QUANT_I8, st, launch_quant_rows(y, d->H, w.yq, w.ys, w.rowlist, M_dev, rows, st));
+  Q8_LAUNCH(TT_K_QUANT_I8, st, launch_quant_rows(y, d->H, w.yq, w.ys, w.rowlist, M_dev, rows, nullptr, st));
   GemmI8Args a{};
   a.M_alloc = rows;
   a.M_dev = M_dev;

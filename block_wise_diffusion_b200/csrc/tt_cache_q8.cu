@@ -131,11 +131,14 @@ constexpr int kQuantThreads = 256, kQuantVec = 4;
 __global__ void __launch_bounds__(kQuantThreads)
     quant_rows_kernel(const uint16_t* __restrict__ x, int K, int8_t* __restrict__ q,
                       float* __restrict__ scale, const int* __restrict__ rowlist,
-                      const int* __restrict__ M_dev, int rows) {
-  griddep_launch();
+                      const int* __restrict__ M_dev, int rows, int* err) {
+  // in this order: what this kernel's dependent reads before its own wait
+  // (weights) is complete when it starts
   griddep_wait();
+  griddep_launch();
   __shared__ uint32_t red[kQuantThreads / 32];
   const int r = blockIdx.x;
+  if (err != nullptr && r == 0 && threadIdx.x < 2) err[threadIdx.x] = 0;
   if (M_dev != nullptr && r >= min(*M_dev, rows)) return;
   const int nv = K >> 3;
   const uint4* src =
@@ -200,9 +203,10 @@ cudaError_t launch_append_q8_len(const AppendQ8Args& a, cudaStream_t st) {
 }
 
 cudaError_t launch_quant_rows(const uint16_t* x, int K, int8_t* q, float* scale,
-                              const int* rowlist, const int* M_dev, int rows, cudaStream_t st) {
+                              const int* rowlist, const int* M_dev, int rows, int* err,
+                              cudaStream_t st) {
   return launch_k(quant_rows_kernel, dim3(rows), dim3(kQuantThreads), 0, st, x, K, q, scale,
-                  rowlist, M_dev, rows);
+                  rowlist, M_dev, rows, err);
 }
 
 }  // namespace tt

@@ -22,8 +22,10 @@ cudaError_t launch_append_q8_len(const AppendQ8Args& a, cudaStream_t st);
 
 // Row r < rows (or < *M_dev) of x, or row rowlist[r] of it: int8 codes q[r, :]
 // and scale[r].
+// err: an error word to clear first (optional).
 cudaError_t launch_quant_rows(const uint16_t* x, int K, int8_t* q, float* scale,
-                              const int* rowlist, const int* M_dev, int rows, cudaStream_t st);
+                              const int* rowlist, const int* M_dev, int rows, int* err,
+                              cudaStream_t st);
 
 // ------------------------------------------------------- integer products
 // C = A[M, K] . B[N, K]^T, both int8 and K-major, 128 rows x 128 bytes of K
@@ -46,6 +48,10 @@ cudaError_t launch_gemm_i8_vocab(const CUtensorMap& tmA, const CUtensorMap& tmB,
                                  const GemmI8Args& a, int grid, cudaStream_t st);
 cudaError_t launch_gemm_i8_linear(const CUtensorMap& tmA, const CUtensorMap& tmB,
                                   const GemmI8Args& a, int grid, cudaStream_t st);
+// Few tiles: `splits` (a power of two, at most 8) CTAs to a 128 x 128 tile.
+constexpr int kI8SplitBN = 128, kI8MaxSplits = 8;
+cudaError_t launch_gemm_i8_split(const CUtensorMap& tmA, const CUtensorMap& tmB,
+                                 const GemmI8Args& a, int splits, cudaStream_t st);
 
 // --------------------------------------------------------------- attention
 // Units, query tiles and the partition of key tiles are those of the bf16
