@@ -136,6 +136,38 @@ LinearWs carve_linear(int rows, int K, void* ws) {
   return w;
 }
 
+// Tile width and K split of the linear update.  Where 128-row tiles of 32, 64 or
+// 128 columns are no more than the SMs, each tile goes to a cluster of `splits`
+// CTAs that share its K: of the shapes that fit, the one whose CTAs read the
+// fewest bytes, an exchange of partial sums counted as 200 KB (about 1 us).
+// 128 x 4608, K = 4096: 72 tiles of 64 in pairs 11.2 us, 144 of 32 alone 12.8,
+// 36 of 128 in fours 17.3 (clusters of four leave SMs of a GPC over, so not
+// all 36 run at once: more than two CTAs only within 7/8 of the SMs).
+// splits = 0: more tiles than SMs; 256-wide tiles, one CTA each in turn, which
+// read A less often.
+struct I8Shape {
+  int bn, splits;
+};
+I8Shape i8_shape(int rows, int N, int K) {
+  const long long m_tiles = (rows + kI8BM - 1ll) / kI8BM;
+  const int sms = num_sms(), nkb = (K + kI8BK - 1) / kI8BK;
+  I8Shape best{kI8BN, 0};
+  double least = 0;
+  for (int bn = 32; bn <= 128; bn *= 2) {
+    const long long tiles = m_tiles * ((N + bn - 1ll) / bn);
+    if (tiles > sms) continue;
+    int s = 1;
+    while (2 * s <= bn / 16 && 4 * s <= nkb && tiles * 2 * s <= (s == 1 ? sms : sms * 7 / 8))
+      s *= 2;
+    const double bytes = (double)K / s * (kI8BM + bn) + (s > 1 ? 200e3 : 0);
+    if (best.splits == 0 || bytes < least) {
+      best = I8Shape{bn, s};
+      least = bytes;
+    }
+  }
+  return best;
+}
+
 constexpr int kMaxRows = 1 << 24, kMaxK = 131072;
 tt_status check_rows_k(int rows, int K) {
   if (rows < 1) return set_errorf(TT_ERR_INVALID_ARG, "rows=%d", rows);
@@ -315,24 +347,15 @@ tt_status tt_linear_i8(int32_t rows, int32_t N, int32_t K, const tt_bf16* x, con
   const LinearWs w = carve_linear(rows, K, ws);
   Q8_CHECK(check_ws_ptr(ws, ws_bytes, w.total));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  // Fewer 128-wide tiles than SMs: each is shared by a cluster that splits K
-  // (128 x 4608, K = 4096: 36 tiles of 4 CTAs, @@ us against 22 us on 18 SMs
-  // with 256-wide tiles).  Otherwise 256-wide tiles, one CTA each in turn,
-  // which read A half as often.
-  const long long m_tiles = (rows + kI8BM - 1ll) / kI8BM;
-  const long long tiles128 = m_tiles * ((N + kI8SplitBN - 1ll) / kI8SplitBN);
-  const int sms = num_sms(), nkb = (K + kI8BK - 1) / kI8BK;
-  int splits = 0;
-  if (tiles128 <= sms) {
-    splits = 1;
-    while (splits < kI8MaxSplits && 2 * splits <= nkb && tiles128 * 2 * splits <= sms) splits *= 2;
-  }
+  const I8Shape sh = i8_shape(rows, N, K);
   CUtensorMap tmA, tmB;
-  if (!make_tmap_2d_u8(&tmA, w.xq, K, rows, K, kI8BK, kI8BM) ||
-      !make_tmap_2d_u8(&tmB, w_q, K, N, K, kI8BK, splits ? kI8SplitBN : kI8BN))
+  const int a_box = std::min(rows, kI8BM);
+  if (!make_tmap_2d_u8(&tmA, w.xq, K, rows, K, kI8BK, a_box) ||
+      !make_tmap_2d_u8(&tmB, w_q, K, N, K, kI8BK, sh.bn))
     return set_errorf(TT_ERR_CUDA, "cuTensorMapEncodeTiled failed for the 8-bit linear update");
   GemmI8Args a{};
   a.M_alloc = rows;
+  a.a_box = a_box;
   a.N = N;
   a.K = K;
   a.a_scale = w.xs;
@@ -341,12 +364,13 @@ tt_status tt_linear_i8(int32_t rows, int32_t N, int32_t K, const tt_bf16* x, con
   a.err = w.ctrl;
   Q8_LAUNCH(TT_K_QUANT_I8, st,
             launch_quant_rows(x, K, w.xq, w.xs, nullptr, nullptr, rows, w.ctrl, st));
-  if (splits) {
-    Q8_LAUNCH(TT_K_GEMM_I8, st, launch_gemm_i8_split(tmA, tmB, a, splits, st));
+  if (sh.splits) {
+    Q8_LAUNCH(TT_K_GEMM_I8, st, launch_gemm_i8_split(tmA, tmB, a, sh.bn, sh.splits, st));
   } else {
-    const long long tiles = m_tiles * ((N + kI8BN - 1ll) / kI8BN);
+    const long long tiles =
+        ((rows + kI8BM - 1ll) / kI8BM) * ((N + kI8BN - 1ll) / kI8BN);
     Q8_LAUNCH(TT_K_GEMM_I8, st,
-              launch_gemm_i8_linear(tmA, tmB, a, (int)std::min<long long>(tiles, sms), st));
+              launch_gemm_i8_linear(tmA, tmB, a, (int)std::min<long long>(tiles, num_sms()), st));
   }
   return TT_OK;
 }
@@ -365,15 +389,26 @@ tt_status tt_vocab_confidence_commit_i8(const tt_dims* d, const tt_bf16* y, cons
   const int rows = d->B * d->S;
   const int* M_dev = w.ctrl + CTRL_M;
   CUtensorMap tmA, tmB;
-  if (!make_tmap_2d_u8(&tmA, w.yq, d->H, rows, d->H, kI8BK, kI8BM) ||
+  const int a_box = std::min(rows, kI8BM);
+  if (!make_tmap_2d_u8(&tmA, w.yq, d->H, rows, d->H, kI8BK, a_box) ||
       !make_tmap_2d_u8(&tmB, w_q, d->H, d->V, d->H, kI8BK, kI8VocabBN))
     return set_errorf(TT_ERR_CUDA, "cuTensorMapEncodeTiled failed for the 8-bit vocabulary GEMM");
-  Q8_CUDA(cudaMemsetAsync(w.ctrl, 0, w.clear, st));
-  PlanArgs p{d->B, d->S, masked, w.rowlist, w.tvec, w.ctrl, 0};
-  Q8_LAUNCH(TT_K_PLAN, st, launch_plan(p, st));
-  Q8_LAUNCH(TT_K_QUANT_I8, st, launch_quant_rows(y, d->H, w.yq, w.ys, w.rowlist, M_dev, rows, nullptr, st));
+  // Each row counts the masked rows before it; beyond some thousands of rows
+  // (32 MB of flags read for 8192) a plan does it once instead.
+  if (rows <= 8192) {
+    Q8_LAUNCH(TT_K_QUANT_I8, st,
+              launch_masked_rows(y, d->H, w.yq, w.ys, masked, rows, d->S, w.rowlist, w.ctrl,
+                                 w.seqcnt, st));
+  } else {
+    Q8_CUDA(cudaMemsetAsync(w.ctrl, 0, w.clear, st));
+    PlanArgs p{d->B, d->S, masked, w.rowlist, w.tvec, w.ctrl, 0};
+    Q8_LAUNCH(TT_K_PLAN, st, launch_plan(p, st));
+    Q8_LAUNCH(TT_K_QUANT_I8, st,
+              launch_quant_rows(y, d->H, w.yq, w.ys, w.rowlist, M_dev, rows, nullptr, st));
+  }
   GemmI8Args a{};
   a.M_alloc = rows;
+  a.a_box = a_box;
   a.M_dev = M_dev;
   a.N = d->V;
   a.K = d->H;

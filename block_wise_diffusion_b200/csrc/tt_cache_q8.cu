@@ -124,26 +124,13 @@ __global__ void __launch_bounds__(256) append_len_kernel(const AppendQ8Args a) {
   }
 }
 
-// Row r of x (row rowlist[r] of it with a row list) to int8 codes and a
-// scale.  One CTA per row; a row of up to 8192 values stays in registers, a
-// longer one is read again (from L2).
+// A row of K values to int8 codes and a scale, by the whole CTA.  A row of up
+// to 8192 values stays in registers, a longer one is read again (from L2).
 constexpr int kQuantThreads = 256, kQuantVec = 4;
-__global__ void __launch_bounds__(kQuantThreads)
-    quant_rows_kernel(const uint16_t* __restrict__ x, int K, int8_t* __restrict__ q,
-                      float* __restrict__ scale, const int* __restrict__ rowlist,
-                      const int* __restrict__ M_dev, int rows, int* err) {
-  // in this order: what this kernel's dependent reads before its own wait
-  // (weights) is complete when it starts
-  griddep_wait();
-  griddep_launch();
+__device__ __forceinline__ void quant_row(const uint4* __restrict__ src, int K,
+                                          uint2* __restrict__ dst, float* __restrict__ scale) {
   __shared__ uint32_t red[kQuantThreads / 32];
-  const int r = blockIdx.x;
-  if (err != nullptr && r == 0 && threadIdx.x < 2) err[threadIdx.x] = 0;
-  if (M_dev != nullptr && r >= min(*M_dev, rows)) return;
   const int nv = K >> 3;
-  const uint4* src =
-      reinterpret_cast<const uint4*>(x + (long long)(rowlist != nullptr ? rowlist[r] : r) * K);
-  uint2* dst = reinterpret_cast<uint2*>(q + (long long)r * K);
   uint4 v[kQuantVec];
   uint32_t mx = 0;
 #pragma unroll
@@ -171,7 +158,56 @@ __global__ void __launch_bounds__(kQuantThreads)
   }
   for (int i = kQuantVec * kQuantThreads + threadIdx.x; i < nv; i += kQuantThreads)
     dst[i] = ok ? q8_pack8<TT_Q8_INT8>(src[i], s, inv) : make_uint2(0, 0);
-  if (threadIdx.x == 0) scale[r] = s;
+  if (threadIdx.x == 0) *scale = s;
+}
+
+// CTA r: row r of x (row rowlist[r] of it with a row list, *M_dev rows).
+// These kernels wait before they let their dependent start: what that reads
+// before its own wait (weights) is complete then.
+__global__ void __launch_bounds__(kQuantThreads)
+    quant_rows_kernel(const uint16_t* __restrict__ x, int K, int8_t* __restrict__ q,
+                      float* __restrict__ scale, const int* __restrict__ rowlist,
+                      const int* __restrict__ M_dev, int rows, int* err) {
+  griddep_wait();
+  griddep_launch();
+  const int r = blockIdx.x;
+  if (err != nullptr && r == 0 && threadIdx.x < 2) err[threadIdx.x] = 0;
+  if (M_dev != nullptr && r >= min(*M_dev, rows)) return;
+  quant_row(reinterpret_cast<const uint4*>(x + (long long)(rowlist != nullptr ? rowlist[r] : r) * K),
+            K, reinterpret_cast<uint2*>(q + (long long)r * K), scale + r);
+}
+
+// The vocabulary step's rows without a planning launch: CTA r finds the place of
+// its masked row among the masked rows by counting those before it, and
+// quantises it there.  Also what a plan would leave: the row lists, the row
+// count (the last CTA), cleared error words and commit counters.
+__global__ void __launch_bounds__(kQuantThreads)
+    masked_rows_kernel(const uint16_t* __restrict__ x, int K, int8_t* __restrict__ q,
+                       float* __restrict__ scale, const uint8_t* __restrict__ masked, int rows,
+                       int S, int* __restrict__ rowlist, int* __restrict__ ctrl,
+                       int* __restrict__ seqcnt) {
+  griddep_wait();
+  griddep_launch();
+  const int r = blockIdx.x;
+  if (r == 0 && threadIdx.x < 2) ctrl[threadIdx.x] = 0;
+  if (threadIdx.x == 0 && r % S == 0) seqcnt[r / S] = 0;
+  const int mine = masked[r] != 0;
+  if (!mine && r != rows - 1) return;
+  int j = 0;
+  for (int i0 = 0; i0 < r; i0 += kQuantThreads) {
+    const int i = i0 + threadIdx.x;
+    j += __syncthreads_count(i < r && masked[i] != 0);
+  }
+  if (threadIdx.x == 0) {
+    if (r == rows - 1) ctrl[CTRL_M] = j + mine;
+    if (mine) {
+      rowlist[j] = r;
+      rowlist[rows + r] = j;
+    }
+  }
+  if (mine)
+    quant_row(reinterpret_cast<const uint4*>(x + (long long)r * K), K,
+              reinterpret_cast<uint2*>(q + (long long)j * K), scale + j);
 }
 
 }  // namespace
@@ -207,6 +243,13 @@ cudaError_t launch_quant_rows(const uint16_t* x, int K, int8_t* q, float* scale,
                               cudaStream_t st) {
   return launch_k(quant_rows_kernel, dim3(rows), dim3(kQuantThreads), 0, st, x, K, q, scale,
                   rowlist, M_dev, rows, err);
+}
+
+cudaError_t launch_masked_rows(const uint16_t* x, int K, int8_t* q, float* scale,
+                               const uint8_t* masked, int rows, int S, int* rowlist, int* ctrl,
+                               int* seqcnt, cudaStream_t st) {
+  return launch_k(masked_rows_kernel, dim3(rows), dim3(kQuantThreads), 0, st, x, K, q, scale,
+                  masked, rows, S, rowlist, ctrl, seqcnt);
 }
 
 }  // namespace tt

@@ -90,6 +90,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   // With one row tile a CTA's first tile does not depend on the row count:
   // its first B stages are requested before the rows of A are ready.
   const int early = a.M_alloc <= kI8BM ? min(nkb, STAGES) : 0;
+  const uint32_t a_bytes = (uint32_t)a.a_box * kI8BK;
 
   uint8_t* base = align1024(smem_raw);
   uint8_t* sA = base;
@@ -101,7 +102,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acce + 2);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (the shuffle tells the compiler that the index is the same in all lanes)
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&full[s], 1);
@@ -125,7 +127,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   if (warp == 0 && lane == 0 && early > 0) {
     const uint64_t once = policy_evict_first();
     for (int kb = 0; kb < early; ++kb) {
-      mbar_arrive_expect_tx(&full[kb], kStageA + kStageB);
+      mbar_arrive_expect_tx(&full[kb], a_bytes + kStageB);
       tma_load_2d_hint(sB + kb * kStageB, &tmB, &full[kb], kb * kI8BK, blockIdx.x * BN, once);
     }
   }
@@ -158,7 +160,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             ok = false;
             break;
           }
-          if (ahead == 0) mbar_arrive_expect_tx(&full[stage], kStageA + kStageB);
+          if (ahead == 0) mbar_arrive_expect_tx(&full[stage], a_bytes + kStageB);
           tma_load_2d_hint(sA + stage * kStageA, &tmA, &full[stage], kb * kI8BK, m * kI8BM, keep);
           if (ahead == 0)
             tma_load_2d_hint(sB + stage * kStageB, &tmB, &full[stage], kb * kI8BK, n * BN,
@@ -188,7 +190,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           break;
         }
         tc_fence_after();
-        if (lane == 0) {
+        if (elect_one()) {
           const uint64_t a0 = sdesc_sw128(smem_u32(sA + stage * kStageA), 16, 1024);
           const uint64_t b0 = sdesc_sw128(smem_u32(sB + stage * kStageB), 16, 1024);
 #pragma unroll
@@ -203,7 +205,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         }
       }
       if (!ok) break;
-      if (lane == 0) umma_commit(&accf[acc]);
+      if (elect_one()) umma_commit(&accf[acc]);
       __syncwarp();
       acc ^= 1;
       if (acc == 0) acc_phase ^= 1;
@@ -295,12 +297,17 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   }
 }
 
-// A cluster's CTAs each take a range of K of one 128 x 128 tile.
-constexpr int kSplitBN = 128, kSplitStages = 5;
-constexpr uint32_t kSplitStageB = kSplitBN * kI8BK;
-// partial sums of the other CTAs for this one's columns: [source][column
-// group of 4][128 rows][4]; at most 7/8 of a 64 KB tile
-constexpr uint32_t kSplitRecv = 128 * kSplitBN * 4 * 7 / 8;
+// One 128 x BN tile to a cluster, whose CTAs each take a range of K (splits = 1:
+// to a CTA).
+template <int BN>
+struct SplitShape {
+  static constexpr int kStages = BN == 128 ? 5 : BN == 64 ? 7 : 9;
+  static constexpr uint32_t kStageB = BN * kI8BK;
+  // partial sums of the other CTAs for this one's columns: [source][column
+  // group of 4][128 rows][4]; splits <= BN / 16
+  static constexpr uint32_t kRecv = 128 * BN * 4 * (BN / 16 - 1) / (BN / 16);
+  static constexpr size_t kSmem = kStages * (kStageA + kStageB) + kRecv + 1024 + 256;
+};
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -321,29 +328,35 @@ __device__ __forceinline__ void st_cluster(uint32_t saddr, uint32_t rank, uint32
                : "memory");
 }
 
+template <int BN>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     gemm_i8_split_kernel(const __grid_constant__ CUtensorMap tmA,
                          const __grid_constant__ CUtensorMap tmB, const GemmI8Args a,
                          const int splits) {
   griddep_launch();
+  using Shape = SplitShape<BN>;
+  constexpr int STAGES = Shape::kStages;
+  constexpr uint32_t kStageB = Shape::kStageB;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = align1024(smem_raw);
   uint8_t* sA = base;
-  uint8_t* sB = base + kSplitStages * kStageA;
-  uint8_t* recv = sB + kSplitStages * kSplitStageB;
-  uint64_t* full = reinterpret_cast<uint64_t*>(recv + kSplitRecv);
-  uint64_t* empty = full + kSplitStages;
-  uint64_t* accf = empty + kSplitStages;
+  uint8_t* sB = base + STAGES * kStageA;
+  uint8_t* recv = sB + STAGES * kStageB;
+  uint64_t* full = reinterpret_cast<uint64_t*>(recv + Shape::kRecv);
+  uint64_t* empty = full + STAGES;
+  uint64_t* accf = empty + STAGES;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(accf + 1);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (the shuffle tells the compiler that the index is the same in all lanes)
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int rank = splits > 1 ? (int)cluster_rank() : 0;
   const int num_m = (a.M_alloc + kI8BM - 1) / kI8BM;
   const int tile = blockIdx.x / splits, m = tile % num_m, n = tile / num_m;
   const int nkb = (a.K + kI8BK - 1) / kI8BK;
   const int kb0 = rank * nkb / splits, kb1 = (rank + 1) * nkb / splits;
+  const uint32_t a_bytes = (uint32_t)a.a_box * kI8BK;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kSplitStages; ++s) {
+    for (int s = 0; s < STAGES; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
@@ -363,11 +376,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   if (warp == 0) {
     if (lane == 0) {
       const uint64_t keep = policy_evict_last();
-      // (a fresh ring: the first kSplitStages stages need no wait)
-      const int early = min(kb1 - kb0, kSplitStages);
+      // (a fresh ring: the first STAGES stages need no wait)
+      const int early = min(kb1 - kb0, STAGES);
       for (int i = 0; i < early; ++i) {
-        mbar_arrive_expect_tx(&full[i], kStageA + kSplitStageB);
-        tma_load_2d_hint(sB + i * kSplitStageB, &tmB, &full[i], (kb0 + i) * kI8BK, n * kSplitBN, keep);
+        mbar_arrive_expect_tx(&full[i], a_bytes + kStageB);
+        tma_load_2d_hint(sB + i * kStageB, &tmB, &full[i], (kb0 + i) * kI8BK, n * BN, keep);
       }
       griddep_wait();
       int stage = 0;
@@ -375,19 +388,19 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       for (int kb = kb0; kb < kb1; ++kb) {
         if (!mbar_wait(&empty[stage], phase ^ 1, a.err, abort_flag, WHERE_GEMM_PRODUCER)) break;
         if (kb - kb0 >= early) {
-          mbar_arrive_expect_tx(&full[stage], kStageA + kSplitStageB);
-          tma_load_2d_hint(sB + stage * kSplitStageB, &tmB, &full[stage], kb * kI8BK, n * kSplitBN,
+          mbar_arrive_expect_tx(&full[stage], a_bytes + kStageB);
+          tma_load_2d_hint(sB + stage * kStageB, &tmB, &full[stage], kb * kI8BK, n * BN,
                            keep);
         }
         tma_load_2d_hint(sA + stage * kStageA, &tmA, &full[stage], kb * kI8BK, m * kI8BM, keep);
-        if (++stage == kSplitStages) {
+        if (++stage == STAGES) {
           stage = 0;
           phase ^= 1;
         }
       }
     }
   } else if (warp == 1) {
-    constexpr uint32_t idesc = idesc_i8(kI8BM, kSplitBN);
+    constexpr uint32_t idesc = idesc_i8(kI8BM, BN);
     int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
@@ -397,31 +410,31 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         break;
       }
       tc_fence_after();
-      if (lane == 0) {
+      if (elect_one()) {
         const uint64_t a0 = sdesc_sw128(smem_u32(sA + stage * kStageA), 16, 1024);
-        const uint64_t b0 = sdesc_sw128(smem_u32(sB + stage * kSplitStageB), 16, 1024);
+        const uint64_t b0 = sdesc_sw128(smem_u32(sB + stage * kStageB), 16, 1024);
 #pragma unroll
         for (int k = 0; k < kI8BK / 32; ++k)
           umma_i8_ss(tmem, a0 + k * 2, b0 + k * 2, idesc, (kb > kb0 || k > 0) ? 1u : 0u);
         umma_commit(&empty[stage]);
       }
       __syncwarp();
-      if (++stage == kSplitStages) {
+      if (++stage == STAGES) {
         stage = 0;
         phase ^= 1;
       }
     }
-    if (ok && lane == 0) umma_commit(accf);
+    if (ok && elect_one()) umma_commit(accf);
     __syncwarp();
   }
   const int q = warp & 3, row128 = q * 32 + lane;
   const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16);
-  const int part = kSplitBN / splits;  // columns this CTA finishes: rank * part ..
+  const int part = BN / splits;  // columns this CTA finishes: rank * part ..
   bool ok = warp >= 2 && mbar_wait(accf, 0, a.err, abort_flag, WHERE_GEMM_EPI);
   if (ok) tc_fence_after();
   if (ok && splits > 1) {
 #pragma unroll 1
-    for (int c0 = 0; c0 < kSplitBN; c0 += 16) {
+    for (int c0 = 0; c0 < BN; c0 += 16) {
       const int to = c0 / part;
       if (to == rank) continue;
       uint32_t r[16];
@@ -453,7 +466,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     const float rs = row < a.M_alloc ? a.a_scale[row] : 0.f;
 #pragma unroll 1
     for (int c0 = 0; c0 < part; c0 += 32) {
-      const int col = n * kSplitBN + rank * part + c0;
+      const int col = n * BN + rank * part + c0;
       const int lim = min(min(32, part - c0), a.N - col);
       if (lim <= 0) break;
       uint32_t r[32];
@@ -509,14 +522,18 @@ cudaError_t launch_gemm_i8_linear(const CUtensorMap& tmA, const CUtensorMap& tmB
   return launch_gemm_i8<1, kI8BN, kI8Stages>(tmA, tmB, a, grid, st);
 }
 
-cudaError_t launch_gemm_i8_split(const CUtensorMap& tmA, const CUtensorMap& tmB,
-                                 const GemmI8Args& a, int splits, cudaStream_t st) {
-  constexpr size_t smem = kSplitStages * (kStageA + kSplitStageB) + kSplitRecv + 1024 + 256;
+template <int BN>
+static cudaError_t launch_split(const CUtensorMap& tmA, const CUtensorMap& tmB,
+                                const GemmI8Args& a, int splits, cudaStream_t st) {
+  constexpr size_t smem = SplitShape<BN>::kSmem;
   static_assert(smem <= 232448, "shared memory per CTA");
-  cudaError_t e = cudaFuncSetAttribute(gemm_i8_split_kernel,
+  cudaError_t e = cudaFuncSetAttribute(gemm_i8_split_kernel<BN>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  const int tiles = ((a.M_alloc + kI8BM - 1) / kI8BM) * ((a.N + kSplitBN - 1) / kSplitBN);
+  const int tiles = ((a.M_alloc + kI8BM - 1) / kI8BM) * ((a.N + BN - 1) / BN);
+  if (splits == 1)
+    return launch_k(gemm_i8_split_kernel<BN>, dim3(tiles), dim3(kGemmThreads), smem, st, tmA, tmB,
+                    a, 1);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(tiles * splits);
   cfg.blockDim = dim3(kGemmThreads);
@@ -531,9 +548,15 @@ cudaError_t launch_gemm_i8_split(const CUtensorMap& tmA, const CUtensorMap& tmB,
   at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 2;
-  e = cudaLaunchKernelEx(&cfg, gemm_i8_split_kernel, tmA, tmB, a, splits);
+  e = cudaLaunchKernelEx(&cfg, gemm_i8_split_kernel<BN>, tmA, tmB, a, splits);
   count_launch();
   return e;
+}
+cudaError_t launch_gemm_i8_split(const CUtensorMap& tmA, const CUtensorMap& tmB,
+                                 const GemmI8Args& a, int bn, int splits, cudaStream_t st) {
+  if (bn == 32) return launch_split<32>(tmA, tmB, a, splits, st);
+  if (bn == 64) return launch_split<64>(tmA, tmB, a, splits, st);
+  return launch_split<128>(tmA, tmB, a, splits, st);
 }
 
 }  // namespace tt

@@ -27,6 +27,12 @@ cudaError_t launch_quant_rows(const uint16_t* x, int K, int8_t* q, float* scale,
                               const int* rowlist, const int* M_dev, int rows, int* err,
                               cudaStream_t st);
 
+// The masked rows of x, compacted and quantised; writes rowlist (as PlanArgs
+// has it), ctrl[CTRL_M], and clears the error words and seqcnt[0 .. rows / S).
+cudaError_t launch_masked_rows(const uint16_t* x, int K, int8_t* q, float* scale,
+                               const uint8_t* masked, int rows, int S, int* rowlist, int* ctrl,
+                               int* seqcnt, cudaStream_t st);
+
 // ------------------------------------------------------- integer products
 // C = A[M, K] . B[N, K]^T, both int8 and K-major, 128 rows x 128 bytes of K
 // per tile.
@@ -35,6 +41,8 @@ constexpr int kI8VocabBN = kVocabBN, kI8VocabStages = 5;
 constexpr int kI8BN = 256, kI8Stages = 4;
 struct GemmI8Args {
   int M_alloc;           // rows of A
+  int a_box;             // rows of a TMA box of A: fewer than 128 when A has fewer (the
+                         // tile's other rows stay as they are and are never stored)
   const int* M_dev;      // device row count (nullptr: M_alloc)
   int N, K;
   const float* a_scale;  // [M]
@@ -48,10 +56,10 @@ cudaError_t launch_gemm_i8_vocab(const CUtensorMap& tmA, const CUtensorMap& tmB,
                                  const GemmI8Args& a, int grid, cudaStream_t st);
 cudaError_t launch_gemm_i8_linear(const CUtensorMap& tmA, const CUtensorMap& tmB,
                                   const GemmI8Args& a, int grid, cudaStream_t st);
-// Few tiles: `splits` (a power of two, at most 8) CTAs to a 128 x 128 tile.
-constexpr int kI8SplitBN = 128, kI8MaxSplits = 8;
+// Few tiles: `splits` CTAs (a power of two, at most bn / 16) to a 128 x bn tile,
+// bn 32, 64 or 128.
 cudaError_t launch_gemm_i8_split(const CUtensorMap& tmA, const CUtensorMap& tmB,
-                                 const GemmI8Args& a, int splits, cudaStream_t st);
+                                 const GemmI8Args& a, int bn, int splits, cudaStream_t st);
 
 // --------------------------------------------------------------- attention
 // Units, query tiles and the partition of key tiles are those of the bf16

@@ -193,6 +193,20 @@ def test_vocab_matches_oracle(B, S, Hh, V, gamma, scale):
     assert skipped <= max(1, B // 8), skipped
 
 
+def test_vocab_many_rows():
+    """More rows than the fused planning takes (8192): the same commit rule."""
+    rng = np.random.default_rng(9)
+    masked = (rng.random((520, 16)) < 0.5).astype(np.uint8)
+    got = vocab(520, 16, 64, 300, 0.4, 6.0, 10, masked=masked)
+    assert check_vocab(*got, 0.4, 6.0) <= 4
+
+
+def test_vocab_nothing_masked():
+    got, ref, tokens, m = vocab(2, 16, 128, 300, 0.9, 1.0, 3, masked=np.zeros((2, 16), np.uint8))
+    assert got["status"] == 0 and (got["n"] == 0).all() and (got["conf"] == -1).all()
+    np.testing.assert_array_equal(got["tokens"], tokens)
+
+
 def test_vocab_full_size():
     """The mid-size vocabulary step, 16 rows against the oracle."""
     masked = np.zeros((4, 16), np.uint8)
