@@ -74,7 +74,8 @@ struct Carver {
 
 // -------------------------------------------------------------- attention
 struct AttnQ8Ws {
-  int *ctrl, *seq_start;
+  int* ctrl;
+  int2* unit_span;
   float *part_o, *part_ml;
   size_t total;
 };
@@ -84,7 +85,7 @@ AttnQ8Ws carve_attn(const tt_dims& d, const AttnShape& g, void* ws) {
   const size_t rows = d.S * g.G <= kRowsMax ? kRowsMax : 256;
   const size_t slots = (size_t)g.units + g.n_ctas - 1;
   w.ctrl = c.take<int>(kCtrlBytes);
-  w.seq_start = c.take<int>((size_t)(d.B + 1) * sizeof(int));
+  w.unit_span = c.take<int2>((size_t)g.units * sizeof(int2));
   w.part_o = c.take<float>(slots * rows * d.dh * sizeof(float));
   w.part_ml = c.take<float>(slots * rows * 2 * sizeof(float));
   w.total = c.total();
@@ -257,7 +258,7 @@ tt_status tt_block_denoise_attn_q8(const tt_dims* d, const tt_q8* f, const tt_bf
   a.n_qtiles = g.n_qtiles;
   a.units = g.units;
   a.n_ctas = g.n_ctas;
-  a.seq_start = w.seq_start;
+  a.unit_span = w.unit_span;
   a.part_o = w.part_o;
   a.part_ml = w.part_ml;
   a.err = w.ctrl;

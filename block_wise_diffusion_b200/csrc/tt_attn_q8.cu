@@ -426,7 +426,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
       // segments leave a partial: unnormalised O (tile-major [dh/4][256
       // rows][4], a warp's store is 512 contiguous bytes) and (m, l).
       const int r256 = ch * 128 + r;
-      const bool whole = !split && sa == 0 && sb == 1 + (L + kAttnBN - 1) / kAttnBN;
+      const bool ends = sb == 1 + (L + kAttnBN - 1) / kAttnBN;
+      const bool whole = !split && sa == 0 && ends;
+      if (threadIdx.x == 0) put_span(a, slot - blockIdx.x, sa == 0, ends);
       if (first < sb) {
         float* po = a.part_o + slot * DH * 256 + (size_t)r256 * 4;
         const float inv = 1.f / l;
@@ -742,7 +744,7 @@ __global__ void __launch_bounds__(256) attn_q8_merge_kernel(const AttnQ8Args a) 
   const int row_blocks = a.halves * 4, ngrp = a.dh / 4, parts = ngrp / (8 * NG);
   const int part = blockIdx.x % parts, rb = blockIdx.x / parts % row_blocks;
   const int u = blockIdx.x / (parts * row_blocks);
-  const int2 uc = unit_ctas(a, u);
+  const int2 uc = a.unit_span[u];
   const int per = a.halves == 1 ? 2 : 1;  // records per segment
   if (per == 1 && uc.x == uc.y) return;   // written by its CTA
   const int lane = threadIdx.x & 31, row = rb * 32 + lane, h = row >> 7, r = row & 127;
@@ -804,8 +806,7 @@ template <int TYPE, int DH>
 cudaError_t launch_main(const AttnQ8Args& a, cudaStream_t st) {
   constexpr size_t smem = smem_layout(DH).total + 1024;
   static_assert(smem <= 232448, "shared memory per CTA");
-  cudaError_t e = cudaFuncSetAttribute(attn_q8_kernel<TYPE, DH>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const cudaError_t e = allow_smem<attn_q8_kernel<TYPE, DH>>(smem);
   if (e != cudaSuccess) return e;
   return launch_k(attn_q8_kernel<TYPE, DH>, dim3(a.n_ctas), dim3(kThreads), smem, st, a);
 }

@@ -47,19 +47,14 @@ struct PlanSmem {
   int b, pre;
 };
 
-// First tile of CTA c, floor(c T / P) (P <= 1024: no product leaves 32 bits),
-// and the CTA that holds tile t.
+// First tile of CTA c, floor(c T / P) (P <= 1024: no product leaves 32 bits).
 __device__ __forceinline__ int cta_first(int c, int T, int P) {
   const int base = T / P;
   return c * base + c * (T - base * P) / P;
 }
-__device__ __forceinline__ int tile_cta(int t, int T, int P) {
-  return (int)(((long long)(t + 1) * P - 1) / T);
-}
 
-// Every thread of the CTA: the CTA's walk.  CTA 0 also stores the prefix sums
-// over sequences for the merge, and starts the error word (an out-of-range
-// length is clamped and recorded).  NT: threads of the CTA.
+// Every thread of the CTA: the CTA's walk.  CTA 0 also starts the error word (an
+// out-of-range length is clamped and recorded).  NT: threads of the CTA.
 template <int NT>
 __device__ __forceinline__ TileWalk plan_walk(const AttnQ8Args& a, PlanSmem& sm) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -86,18 +81,9 @@ __device__ __forceinline__ TileWalk plan_walk(const AttnQ8Args& a, PlanSmem& sm)
   int pre = incl - sum + __reduce_add_sync(0xffffffffu, lane < warp ? mine : 0);
   const int U = a.Hkv * a.n_qtiles, T = total * U;
   const int lo = cta_first(blockIdx.x, T, a.n_ctas);
-  if (blockIdx.x == 0) {
-    int p = pre, x = 0;
-#pragma unroll 1
-    for (int b = b0; b < b1; ++b) {
-      a.seq_start[b] = p;
-      p += tiles(b, x);
-    }
-    if (tid == 0) {
-      a.seq_start[a.B] = total;
-      a.err[0] = bad ? (int)TT_ERR_INVALID_ARG : 0;
-      a.err[1] = 0;
-    }
+  if (blockIdx.x == 0 && tid == 0) {
+    a.err[0] = bad ? (int)TT_ERR_INVALID_ARG : 0;
+    a.err[1] = 0;
   }
   if (lo >= pre * U && lo < (pre + sum) * U) {  // exactly one thread
     int b = b0, x = 0;
@@ -130,14 +116,11 @@ __device__ __forceinline__ int tile_keys(int t, int L, int S) {
   return t == 0 ? S : min(kAttnBN, L - (t - 1) * kAttnBN);
 }
 
-// The CTAs that hold a unit's tiles (all of [x, y] have a record, an empty
-// range inside the unit an empty one).
-__device__ __forceinline__ int2 unit_ctas(const AttnQ8Args& a, int u) {
-  const int U = a.Hkv * a.n_qtiles;
-  const int b = u / U, k = u - b * U;
-  const int p0 = a.seq_start[b], n = a.seq_start[b + 1] - p0, T = a.seq_start[a.B] * U;
-  const int s0 = p0 * U + k * n;
-  return make_int2(tile_cta(s0, T, a.n_ctas), tile_cta(s0 + n - 1, T, a.n_ctas));
+// Recorded for the merge by the CTAs that hold a unit's first and last tile: all
+// CTAs between have a record (an empty range inside the unit an empty one).
+__device__ __forceinline__ void put_span(const AttnQ8Args& a, size_t u, bool first, bool last) {
+  if (first) a.unit_span[u].x = blockIdx.x;
+  if (last) a.unit_span[u].y = blockIdx.x;
 }
 
 // 2^e, e in [-126, 127]

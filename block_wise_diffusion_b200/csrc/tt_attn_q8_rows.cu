@@ -24,8 +24,8 @@ namespace tt {
 
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kGroup = 32;          // keys per step of a warp
+constexpr int kWarps = 8, kThreads = kWarps * 32;
+constexpr int NG = 2, kGroup = 16 * NG;  // keys per step of a warp
 constexpr float kRescale = 8.0f;    // log2 units the running maximum may lag
 
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
@@ -187,10 +187,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_rows_kernel(const AttnQ8A
     const uint8_t* vp = a.v_ctx + pair * a.L_cap * DH + (size_t)(2 * c4) * DH + n8 * (DH / 8);
     const float* ksp = a.k_scale + pair * a.n_blocks;
     const float* vsp = a.v_scale + pair * a.n_blocks;
-    uint32_t kr[4][KW], vr[8][VW];
+    uint32_t kr[2 * NG][KW], vr[4 * NG][VW];
     auto load_k = [&](int key0) {
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
+      for (int t = 0; t < 2 * NG; ++t) {
         if (key0 + t * 8 + n8 < key_hi) {
           load_words(kr[t], kp + (size_t)(key0 + t * 8) * DH);
         } else {
@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_rows_kernel(const AttnQ8A
     // vr[4 g + i]: key 16 g + 2 c4 + {0, 1, 8, 9}[i]
     auto load_v = [&](int key0) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < 4 * NG; ++i) {
         const int at = (i >> 2) * 16 + (i & 1) + ((i >> 1) & 1) * 8;
         if (key0 + at + 2 * c4 < key_hi) {
           load_words(vr[i], vp + (size_t)(key0 + at) * DH);
@@ -212,10 +212,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_rows_kernel(const AttnQ8A
         }
       }
     };
-    float nks[2], nvs[2];
+    float nks[NG], nvs[NG];
     auto load_scales = [&](int key0) {
 #pragma unroll
-      for (int g = 0; g < 2; ++g) {
+      for (int g = 0; g < NG; ++g) {
         const int pos = key0 + 16 * g;
         nks[g] = pos < key_hi ? __ldg(ksp + (pos >> a.block_shift)) : 1.f;
         nvs[g] = pos < key_hi ? __ldg(vsp + (pos >> a.block_shift)) : 1.f;
@@ -279,20 +279,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_rows_kernel(const AttnQ8A
     }
     for (; key0 < key_hi; key0 += kWarps * kGroup) {
       const int next = key0 + kWarps * kGroup;
-      float sk[2], lw[2], iw[2];
+      float sk[NG], lw[NG], iw[NG];
 #pragma unroll
-      for (int g = 0; g < 2; ++g) {
+      for (int g = 0; g < NG; ++g) {
         sk[g] = nks[g];
         lw[g] = log2f(nvs[g]);
         iw[g] = 1.f / nvs[g];
       }
-      float s[4][4];
+      float s[2 * NG][4];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
+      for (int t = 0; t < 2 * NG; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
 #pragma unroll
       for (int j = 0; j < KW; ++j)
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
+        for (int t = 0; t < 2 * NG; ++t) {
           uint32_t b0, b1;
           codes4<TYPE>(kr[t][j], b0, b1);
           mma16816(s[t], q[j], b0, b1);
@@ -333,7 +333,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_rows_kernel(const AttnQ8A
     }
     __syncthreads();
     const size_t slot = pair + blockIdx.x;
-    const bool whole = sa == 0 && sb == 1 + (L + kAttnBN - 1) / kAttnBN;
+    const bool ends = sb == 1 + (L + kAttnBN - 1) / kAttnBN, whole = sa == 0 && ends;
+    if (threadIdx.x == 0) put_span(a, pair, sa == 0, ends);
     for (int i = threadIdx.x; i < rows * (DH / 4); i += kThreads) {
       const int r = i / (DH / 4), col = (i - r * (DH / 4)) * 4;
       float mr = -INFINITY;
@@ -366,45 +367,52 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_rows_kernel(const AttnQ8A
   }
 }
 
-// CTA = unit: joins the partial records of a unit that several CTAs hold.
-__global__ void __launch_bounds__(128) attn_q8_rows_merge_kernel(const AttnQ8Args a) {
+// CTA = unit, thread = (row, 4 columns): joins the partial records of a unit that
+// several CTAs hold, the loads of four records in flight together.
+__global__ void __launch_bounds__(512) attn_q8_rows_merge_kernel(const AttnQ8Args a) {
   griddep_launch();
   griddep_wait();
   const int u = blockIdx.x;
-  const int2 uc = unit_ctas(a, u);
+  const int2 uc = a.unit_span[u];
   if (uc.x == uc.y) return;  // written by its CTA
-  const int b = u / a.Hkv, g = u - b * a.Hkv, dv = a.dh / 4;
-  for (int i = threadIdx.x; i < a.rows_per_half * dv; i += 128) {
-    const int r = i / dv, v = i - r * dv;
-    float mr = -INFINITY, den = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c = uc.x; c <= uc.y; ++c) {
-      const size_t slot = (size_t)u + c;
-      const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + slot * 16 + r);
-      if (ml.y == 0.f) continue;
-      const float4 x = __ldcg(reinterpret_cast<const float4*>(a.part_o) + (slot * 16 + r) * dv + v);
-      const float mn = ml.x > mr ? ml.x : mr;
-      const float f0 = ex2(mr - mn), f1 = ex2(ml.x - mn);
-      mr = mn;
-      den = fmaf(den, f0, ml.y * f1);
-      acc.x = fmaf(acc.x, f0, x.x * f1);
-      acc.y = fmaf(acc.y, f0, x.y * f1);
-      acc.z = fmaf(acc.z, f0, x.z * f1);
-      acc.w = fmaf(acc.w, f0, x.w * f1);
+  const int b = u / a.Hkv, g = u - b * a.Hkv, dv_log = a.dh == 64 ? 4 : 5;
+  const int r = threadIdx.x >> dv_log, v = threadIdx.x & ((1 << dv_log) - 1);
+  if (r >= a.rows_per_half) return;
+  float mr = -INFINITY, den = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int c0 = uc.x; c0 <= uc.y; c0 += 4) {
+    float2 ml[4];
+    float4 x[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const size_t rec = ((size_t)u + min(c0 + k, uc.y)) * 16 + r;
+      ml[k] = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + rec);
+      x[k] = __ldcg(reinterpret_cast<const float4*>(a.part_o) + (rec << dv_log) + v);
     }
-    const float inv = 1.f / den;
-    uint16_t* dst =
-        a.out + (((size_t)b * a.S + r / a.G) * a.Hq + g * a.G + r % a.G) * a.dh + v * 4;
-    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv),
-                                                pack_bf16x2(acc.z * inv, acc.w * inv));
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      // past the last record, or one without keys (its output was never written)
+      if (c0 + k > uc.y || ml[k].y == 0.f) continue;
+      const float mn = ml[k].x > mr ? ml[k].x : mr;
+      const float f0 = ex2(mr - mn), f1 = ex2(ml[k].x - mn);
+      mr = mn;
+      den = fmaf(den, f0, ml[k].y * f1);
+      acc.x = fmaf(acc.x, f0, x[k].x * f1);
+      acc.y = fmaf(acc.y, f0, x[k].y * f1);
+      acc.z = fmaf(acc.z, f0, x[k].z * f1);
+      acc.w = fmaf(acc.w, f0, x[k].w * f1);
+    }
   }
+  const float inv = 1.f / den;
+  uint16_t* dst = a.out + (((size_t)b * a.S + r / a.G) * a.Hq + g * a.G + r % a.G) * a.dh + v * 4;
+  *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv),
+                                              pack_bf16x2(acc.z * inv, acc.w * inv));
 }
 
 template <int TYPE, int DH>
 cudaError_t launch_rows(const AttnQ8Args& a, cudaStream_t st) {
   constexpr size_t smem = (size_t)kWarps * 16 * (DH + 4) * sizeof(float);
-  cudaError_t e = cudaFuncSetAttribute(attn_q8_rows_kernel<TYPE, DH>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const cudaError_t e = allow_smem<attn_q8_rows_kernel<TYPE, DH>>(smem);
   if (e != cudaSuccess) return e;
   return launch_k(attn_q8_rows_kernel<TYPE, DH>, dim3(a.n_ctas), dim3(kThreads), smem, st, a);
 }
@@ -417,7 +425,7 @@ cudaError_t launch_attn_q8_rows(const AttnQ8Args& a, int type, cudaStream_t st) 
   return a.dh == 64 ? launch_rows<TT_Q8_E4M3, 64>(a, st) : launch_rows<TT_Q8_E4M3, 128>(a, st);
 }
 cudaError_t launch_attn_q8_rows_merge(const AttnQ8Args& a, cudaStream_t st) {
-  return launch_k(attn_q8_rows_merge_kernel, dim3((unsigned)a.units), dim3(128), 0, st, a);
+  return launch_k(attn_q8_rows_merge_kernel, dim3((unsigned)a.units), dim3(4 * a.dh), 0, st, a);
 }
 
 }  // namespace tt

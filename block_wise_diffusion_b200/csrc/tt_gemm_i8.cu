@@ -504,8 +504,7 @@ cudaError_t launch_gemm_i8(const CUtensorMap& tmA, const CUtensorMap& tmB, const
   constexpr size_t smem = (size_t)STAGES * (kI8BM + BN) * kI8BK + 1024 + 256;
   static_assert(smem <= 232448, "shared memory per CTA");
   static_assert(2 * BN <= 512, "two accumulators must fit TMEM");
-  cudaError_t e = cudaFuncSetAttribute(gemm_i8_kernel<EPI, BN, STAGES>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const cudaError_t e = allow_smem<gemm_i8_kernel<EPI, BN, STAGES>>(smem);
   if (e != cudaSuccess) return e;
   return launch_k(gemm_i8_kernel<EPI, BN, STAGES>, dim3(grid), dim3(kGemmThreads), smem, st, tmA,
                   tmB, a);
@@ -527,8 +526,7 @@ static cudaError_t launch_split(const CUtensorMap& tmA, const CUtensorMap& tmB,
                                 const GemmI8Args& a, int splits, cudaStream_t st) {
   constexpr size_t smem = SplitShape<BN>::kSmem;
   static_assert(smem <= 232448, "shared memory per CTA");
-  cudaError_t e = cudaFuncSetAttribute(gemm_i8_split_kernel<BN>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const cudaError_t e = allow_smem<gemm_i8_split_kernel<BN>>(smem);
   if (e != cudaSuccess) return e;
   const int tiles = ((a.M_alloc + kI8BM - 1) / kI8BM) * ((a.N + BN - 1) / BN);
   if (splits == 1)
@@ -548,9 +546,8 @@ static cudaError_t launch_split(const CUtensorMap& tmA, const CUtensorMap& tmB,
   at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 2;
-  e = cudaLaunchKernelEx(&cfg, gemm_i8_split_kernel<BN>, tmA, tmB, a, splits);
   count_launch();
-  return e;
+  return cudaLaunchKernelEx(&cfg, gemm_i8_split_kernel<BN>, tmA, tmB, a, splits);
 }
 cudaError_t launch_gemm_i8_split(const CUtensorMap& tmA, const CUtensorMap& tmB,
                                  const GemmI8Args& a, int bn, int splits, cudaStream_t st) {

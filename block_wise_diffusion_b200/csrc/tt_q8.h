@@ -1,8 +1,24 @@
 // Internal definitions of the 8-bit serving operators.
 #pragma once
+#include <atomic>
+
 #include "tt_internal.h"
 
 namespace tt {
+
+// cudaFuncSetAttribute(MaxDynamicSharedMemorySize) once per context: a call
+// of these operators can be shorter than the attribute call is.
+template <auto Kern>
+inline cudaError_t allow_smem(size_t bytes) {
+  static std::atomic<unsigned long long> done{0};  // context it was last set for
+  unsigned long long id = 0;
+  const bool known = current_context_id(&id);
+  if (known && done.load(std::memory_order_relaxed) == id) return cudaSuccess;
+  const cudaError_t e =
+      cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess && known) done.store(id, std::memory_order_relaxed);
+  return e;
+}
 
 // ------------------------------------------------------------ cache append
 struct AppendQ8Args {
@@ -73,7 +89,7 @@ struct AttnQ8Args {
   float scale_log2;  // log2(e) / sqrt(dh)
   uint16_t* out;
   int s_per_half, rows_per_half, halves, n_qtiles, units, n_ctas;
-  int* seq_start;  // [B + 1] key tiles per unit of the sequences before (written by CTA 0)
+  int2* unit_span;  // [units] first and last CTA that hold tiles of the unit
   float* part_o;   // [units + n_ctas - 1] unnormalised outputs of segments:
                    // [dh/4][256 rows][4], or [16 rows][dh] (at most 16 rows)
   float* part_ml;  // [units + n_ctas - 1][256 or 16 rows][2]: maximum (log2 units), sum
