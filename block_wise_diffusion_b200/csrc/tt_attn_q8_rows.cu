@@ -7,8 +7,10 @@
 // global memory straight into the operand registers of warp-level matrix
 // instructions (m16n8k16, fp16): no shared memory and no barrier on the way.
 // That works because the order of dh inside a product is free:
-//   S = Q K^T   lane (n, c) = (lane / 4, lane % 4) loads dh/4 consecutive codes
-//               of key n; its word j is exactly the operand of step j;
+//   S = Q K^T   lane (n, c) = (lane / 4, lane % 4) loads two runs of dh/8 codes
+//               of key n (one from each half of the row, so that the lanes of
+//               a key read whole sectors); its word j is exactly the operand
+//               of step j;
 //   O += P V    lane (n, c) loads dh/8 consecutive codes (columns n dh/8 ..) of
 //               the keys 2c, 2c+1, 2c+8, 2c+9; byte j of a pair of keys is the
 //               operand of column tile j.
@@ -30,27 +32,30 @@ constexpr float kRescale = 8.0f;    // log2 units the running maximum may lag
 
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                          uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// N codes-words from global memory, not kept in L1.
+// N (2 or 4) words of codes from global memory, not kept in L1.
 template <int N>
-__device__ __forceinline__ void load_words(uint32_t (&x)[N], const uint8_t* p) {
-  if constexpr (N == 2) {
+__device__ __forceinline__ void load_words(uint32_t* x, const uint8_t* p) {
+  if constexpr (N == 2)
     asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];"
                  : "=r"(x[0]), "=r"(x[1])
                  : "l"(p));
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; i += 4)
-      asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                   : "=r"(x[i]), "=r"(x[i + 1]), "=r"(x[i + 2]), "=r"(x[i + 3])
-                   : "l"(p + 4 * i));
-  }
+  else
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                 : "l"(p));
+}
+// Where the i-th vector of 8 values of a lane's dh/4 lies: its first run of dh/8
+// is in the first half of the row, the second in the other.
+template <int DH>
+__device__ __forceinline__ constexpr int run_at(int i) {
+  return i < DH / 64 ? 8 * i : DH / 2 + 8 * (i - DH / 64);
 }
 
 template <int TYPE, int DH>
@@ -79,52 +84,26 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_rows_kernel(const AttnQ8A
   int ub, ug, sa, sb, L;
   while (walk.next(ub, ug, sa, sb, L)) {
     const size_t pair = (size_t)ub * a.Hkv + ug;
-    // ---- Q: rows n8 and n8 + 8, each brought into fp16 range by a power of two
     uint32_t q[KW][4];
     float c_row[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int r = n8 + 8 * h;
-      uint4 x[DH / 32];
-      uint32_t mx = 0;
-      // row r = position r / G of the block, head r % G
-      const uint16_t* p = a.q + (((size_t)ub * a.S + r / a.G) * a.Hq + ug * a.G + r % a.G) * DH +
-                          c4 * (DH / 4);
-#pragma unroll
-      for (int i = 0; i < DH / 32; ++i) {
-        x[i] = r < rows ? reinterpret_cast<const uint4*>(p)[i] : make_uint4(0, 0, 0, 0);
-        mx = absmax_bf16x8(mx, x[i]);
-      }
-      mx = max(mx & 0xFFFFu, mx >> 16);
-      mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      const int e = norm_exp(mx);
-      const float f = pow2i(-e);
-      c_row[h] = a.scale_log2 * pow2i(e);
-#pragma unroll
-      for (int i = 0; i < DH / 32; ++i) {
-        q[2 * i][h] = bf16x2_to_f16x2(x[i].x, f);
-        q[2 * i][2 + h] = bf16x2_to_f16x2(x[i].y, f);
-        q[2 * i + 1][h] = bf16x2_to_f16x2(x[i].z, f);
-        q[2 * i + 1][2 + h] = bf16x2_to_f16x2(x[i].w, f);
-      }
-    }
     float o[NT][4];
 #pragma unroll
     for (int j = 0; j < NT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 
     // Softmax of NTILE 8-key tiles of scores (16 keys share a scale) and its
-    // product with V: `vfrag(t16, j, b0, b1)` gives the operand of keys
-    // t16*16.. and column tile j.  nv: valid keys.
+    // product with V: `vfrag(t16, j, b0, b1)` gives the operands of keys
+    // t16*16.. and column tiles j .. j + 3.  nv: valid keys.
     auto finish = [&](auto& s, const float* sk, const float* lw, const float* iw, int nv,
                       auto&& vfrag) {
       constexpr int N16 = sizeof(s) / sizeof(s[0]) / 2;
+      if (nv < 16 * N16) {
 #pragma unroll
-      for (int t = 0; t < 2 * N16; ++t)
+        for (int t = 0; t < 2 * N16; ++t)
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-          if (t * 8 + c4 * 2 + e >= nv) s[t][e] = s[t][2 + e] = -INFINITY;
+          for (int e = 0; e < 2; ++e)
+            if (t * 8 + c4 * 2 + e >= nv) s[t][e] = s[t][2 + e] = -INFINITY;
+      }
       float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
       for (int g = 0; g < N16; ++g)
@@ -173,30 +152,31 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_rows_kernel(const AttnQ8A
           p[2 + h] = pack_f16x2(p2, p3);
         }
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          uint32_t b0, b1;
+        for (int j = 0; j < NT; j += 4) {
+          uint32_t b0[4], b1[4];
           vfrag(g, j, b0, b1);
-          mma16816(o[j], p, b0, b1);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) mma16816(o[j + i], p, b0[i], b1[i]);
         }
       }
     };
 
     // ---- the context keys of the segment, group by group
     const int key_lo = (max(sa, 1) - 1) * kAttnBN, key_hi = min((sb - 1) * kAttnBN, L);
-    const uint8_t* kp = a.k_ctx + pair * a.L_cap * DH + (size_t)n8 * DH + c4 * (DH / 4);
+    const uint8_t* kp = a.k_ctx + pair * a.L_cap * DH + (size_t)n8 * DH + c4 * (DH / 8);
     const uint8_t* vp = a.v_ctx + pair * a.L_cap * DH + (size_t)(2 * c4) * DH + n8 * (DH / 8);
     const float* ksp = a.k_scale + pair * a.n_blocks;
     const float* vsp = a.v_scale + pair * a.n_blocks;
     uint32_t kr[2 * NG][KW], vr[4 * NG][VW];
+    // Keys past the segment's end read its last key instead (their scores are
+    // masked): no branch and no zero fill between the loads.
+    const int kb = key_hi - 1 - n8, vb = key_hi - 1 - 2 * c4;
     auto load_k = [&](int key0) {
 #pragma unroll
       for (int t = 0; t < 2 * NG; ++t) {
-        if (key0 + t * 8 + n8 < key_hi) {
-          load_words(kr[t], kp + (size_t)(key0 + t * 8) * DH);
-        } else {
-#pragma unroll
-          for (int i = 0; i < KW; ++i) kr[t][i] = 0;
-        }
+        const uint8_t* p = kp + (ptrdiff_t)min(key0 + t * 8, kb) * DH;
+        load_words<KW / 2>(&kr[t][0], p);
+        load_words<KW / 2>(&kr[t][KW / 2], p + DH / 2);
       }
     };
     // vr[4 g + i]: key 16 g + 2 c4 + {0, 1, 8, 9}[i]
@@ -204,12 +184,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_rows_kernel(const AttnQ8A
 #pragma unroll
       for (int i = 0; i < 4 * NG; ++i) {
         const int at = (i >> 2) * 16 + (i & 1) + ((i >> 1) & 1) * 8;
-        if (key0 + at + 2 * c4 < key_hi) {
-          load_words(vr[i], vp + (size_t)(key0 + at) * DH);
-        } else {
-#pragma unroll
-          for (int w = 0; w < VW; ++w) vr[i][w] = 0;
-        }
+        load_words<VW>(vr[i], vp + (ptrdiff_t)min(key0 + at, vb) * DH);
       }
     };
     float nks[NG], nvs[NG];
@@ -227,6 +202,35 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_rows_kernel(const AttnQ8A
       load_v(key0);
       load_scales(key0);
     }
+    // ---- Q: rows n8 and n8 + 8, each brought into fp16 range by a power of two
+    // (the first codes are on their way)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int r = n8 + 8 * h;
+      uint4 x[DH / 32];
+      uint32_t mx = 0;
+      // row r = position r / G of the block, head r % G
+      const uint16_t* p = a.q + (((size_t)ub * a.S + r / a.G) * a.Hq + ug * a.G + r % a.G) * DH +
+                          c4 * (DH / 8);
+#pragma unroll
+      for (int i = 0; i < DH / 32; ++i) {
+        x[i] = r < rows ? *reinterpret_cast<const uint4*>(p + run_at<DH>(i)) : make_uint4(0, 0, 0, 0);
+        mx = absmax_bf16x8(mx, x[i]);
+      }
+      mx = max(mx & 0xFFFFu, mx >> 16);
+      mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      const int e = norm_exp(mx);
+      const float f = pow2i(-e);
+      c_row[h] = a.scale_log2 * pow2i(e);
+#pragma unroll
+      for (int i = 0; i < DH / 32; ++i) {
+        q[2 * i][h] = bf16x2_to_f16x2(x[i].x, f);
+        q[2 * i][2 + h] = bf16x2_to_f16x2(x[i].y, f);
+        q[2 * i + 1][h] = bf16x2_to_f16x2(x[i].z, f);
+        q[2 * i + 1][2 + h] = bf16x2_to_f16x2(x[i].w, f);
+      }
+    }
     // ---- the block's own keys (at most 16), by one warp while the others start
     if (sa == 0 && warp == kWarps - 1) {
       const int S = a.S;
@@ -235,10 +239,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_rows_kernel(const AttnQ8A
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         const int key = t * 8 + n8;
-        const uint16_t* p = a.k_blk + (((size_t)ub * S + key) * a.Hkv + ug) * DH + c4 * (DH / 4);
+        const uint16_t* p = a.k_blk + (((size_t)ub * S + key) * a.Hkv + ug) * DH + c4 * (DH / 8);
 #pragma unroll
         for (int i = 0; i < KW / 2; ++i) {
-          const uint4 x = key < S ? reinterpret_cast<const uint4*>(p)[i] : make_uint4(0, 0, 0, 0);
+          const uint4 x =
+              key < S ? *reinterpret_cast<const uint4*>(p + run_at<DH>(i)) : make_uint4(0, 0, 0, 0);
           mk = absmax_bf16x8(mk, x);
           bk[t][4 * i] = x.x, bk[t][4 * i + 1] = x.y, bk[t][4 * i + 2] = x.z, bk[t][4 * i + 3] = x.w;
         }
@@ -267,14 +272,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_rows_kernel(const AttnQ8A
                    bf16x2_to_f16x2(bk[t][2 * j + 1], fk));
       }
       const float sk[1] = {pow2i(ek)}, lw[1] = {(float)ev}, iw[1] = {pow2i(-ev)};
-      finish(s, sk, lw, iw, S, [&](int, int j, uint32_t& b0, uint32_t& b1) {
-        // value j of each key: half a word
-        auto v = [&](int i) {
-          const uint32_t w = bv[i][j >> 1];
-          return __uint_as_float(j & 1 ? w & 0xFFFF0000u : w << 16) * fv;
-        };
-        b0 = pack_f16x2(v(0), v(1));
-        b1 = pack_f16x2(v(2), v(3));
+      finish(s, sk, lw, iw, S, [&](int, int j, uint32_t(&b0)[4], uint32_t(&b1)[4]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          // value j + i of each key: half a word
+          auto v = [&](int k) {
+            const uint32_t w = bv[k][(j + i) >> 1];
+            return __uint_as_float(i & 1 ? w & 0xFFFF0000u : w << 16) * fv;
+          };
+          b0[i] = pack_f16x2(v(0), v(1));
+          b1[i] = pack_f16x2(v(2), v(3));
+        }
       });
     }
     for (; key0 < key_hi; key0 += kWarps * kGroup) {
@@ -301,17 +309,27 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_rows_kernel(const AttnQ8A
         load_k(next);
         load_scales(next);
       }
-      finish(s, sk, lw, iw, key_hi - key0, [&](int g, int j, uint32_t& b0, uint32_t& b1) {
-        // byte j of a pair of keys, for two pairs: (k0, k1, k8, k9) as one word
-        const uint32_t x = __byte_perm(vr[4 * g][j >> 2], vr[4 * g + 1][j >> 2],
-                                       (j & 3) | ((4 + (j & 3)) << 4));
-        const uint32_t y = __byte_perm(vr[4 * g + 2][j >> 2], vr[4 * g + 3][j >> 2],
-                                       (j & 3) | ((4 + (j & 3)) << 4));
-        codes4<TYPE>(__byte_perm(x, y, 0x5410), b0, b1);
+      finish(s, sk, lw, iw, key_hi - key0, [&](int g, int j, uint32_t(&b0)[4], uint32_t(&b1)[4]) {
+        // four codes of a pair of keys, interleaved: (k0, k1) of each column
+        const uint32_t w0 = vr[4 * g][j >> 2], w1 = vr[4 * g + 1][j >> 2];
+        const uint32_t w8 = vr[4 * g + 2][j >> 2], w9 = vr[4 * g + 3][j >> 2];
+        codes4<TYPE>(__byte_perm(w0, w1, 0x5140), b0[0], b0[1]);
+        codes4<TYPE>(__byte_perm(w0, w1, 0x7362), b0[2], b0[3]);
+        codes4<TYPE>(__byte_perm(w8, w9, 0x5140), b1[0], b1[1]);
+        codes4<TYPE>(__byte_perm(w8, w9, 0x7362), b1[2], b1[3]);
       });
       if (next < key_hi) load_v(next);
     }
 
+    // the next unit's first keys to L2, while this one's results are joined
+    if (threadIdx.x < 2 && walk.left > 0) {
+      const int nL = min(max(a.ctx_len[walk.b], 0), a.L_cap);
+      const int nk = min(min(nL, (walk.left - 1) * kAttnBN), kWarps * kGroup);
+      if (nk > 0)
+        prefetch_l2_bulk((threadIdx.x ? a.v_ctx : a.k_ctx) +
+                             ((size_t)walk.b * a.Hkv + walk.k) * a.L_cap * DH,
+                         (uint32_t)nk * DH);
+    }
     // ---- the warps' results: o[j] holds columns (2 c4 + {0, 1}) DH/8 + j of
     // rows n8 (first two) and n8 + 8
 #pragma unroll
