@@ -23,42 +23,46 @@ __device__ __forceinline__ int append_rows(const AppendQ8Args& a, int b, int L) 
   return (m < 0 || m > a.n || L < 0 || L > a.L_cap - m) ? -1 : m;
 }
 
-// CTA (x, y): of the pairs (b, g, K or V) y, y + gridDim.y, .., the x-th group
-// of cache blocks that sequence b's new rows may touch, counted from the block
-// that holds its end.  NT: threads of a block.
+// CTA (x, y): pair x of (b, g, K or V), and of the groups of cache blocks that
+// sequence b's new rows may touch, counted from the block that holds its end,
+// y, y + gridDim.y, ..., so that neighbouring CTAs read neighbouring columns of
+// the same rows.  NT: threads of a block.
 template <int TYPE, int NT, int KV>
-__global__ void __launch_bounds__(NT < 128 ? 128 : NT) append_q8_kernel(const AppendQ8Args a) {
+__global__ void __launch_bounds__(NT < 128 ? 128 : NT, NT == 256 ? 4 : 8) append_q8_kernel(const AppendQ8Args a) {
   constexpr int kCta = NT < 128 ? 128 : NT;
   griddep_launch();
   griddep_wait();
   __shared__ uint32_t red[kCta / 32];
-  const int tid = threadIdx.x % NT, bi = blockIdx.x * (kCta / NT) + threadIdx.x / NT;
-  const int pairs = 2 * a.Hkv * a.B;
-  for (int pair = blockIdx.y; pair < pairs; pair += gridDim.y) {
-    const int is_v = pair & 1, b = (pair >> 1) / a.Hkv, g = (pair >> 1) - b * a.Hkv;
-    const int L = a.ctx_len[b], m = append_rows(a, b, L);
+  const int tid = threadIdx.x % NT;
+  const int pair = blockIdx.x, is_v = pair & 1, b = (pair >> 1) / a.Hkv;
+  const int g = (pair >> 1) - b * a.Hkv;
+  const int L = a.ctx_len[b], m = append_rows(a, b, L);
+  for (int group = blockIdx.y; group < a.groups; group += gridDim.y) {
+    const int bi = group * (kCta / NT) + threadIdx.x / NT;
     const int blk = (max(L, 0) >> a.block_shift) + bi;
     const long long p0 = (long long)blk << a.block_shift;  // first position of the block
     const bool mine = m > 0 && p0 < (long long)L + m;
     if (kCta == NT && !mine) continue;
     const int n_old = mine ? max(0, (int)(L - p0)) : 0;  // older rows in the block
     const int n_end = mine ? (int)min(1ll << a.block_shift, L + m - p0) : 0;
-    const int dv_log = a.dh == 64 ? 3 : 4;              // vectors per row: 8 or 16
-    const int lo = n_old << dv_log, hi = n_end << dv_log;  // new vectors of the block
+    // A thread's vectors: one column of 8 values, rows row0, row0 + step, .. of the
+    // block, of which n_old .. n_end - 1 are new.
+    const int dv_log = a.dh == 64 ? 3 : 4, step = NT >> dv_log;
+    const int row0 = tid >> dv_log, col = tid & ((1 << dv_log) - 1);
     const uint16_t* src = (is_v ? a.v_new : a.k_new) + (long long)b * a.stride_b +
-                          (long long)g * a.stride_h + (p0 - L) * a.stride_t;
+                          (long long)g * a.stride_h + (p0 - L + row0) * a.stride_t + col * 8;
+    const long long src_step = (long long)step * a.stride_t;
     uint4 x[KV];
     uint32_t mx = 0;
 #pragma unroll
     for (int k = 0; k < KV; ++k) {
-      const int i = lo + k * NT + tid;
-      if (i < hi) {
-        const int t = i >> dv_log;
-        x[k] = *reinterpret_cast<const uint4*>(src + (long long)t * a.stride_t +
-                                               (i - (t << dv_log)) * 8);
-        mx = absmax8(mx, x[k]);
-      }
+      const int row = row0 + k * step;
+      x[k] = make_uint4(0, 0, 0, 0);
+      if (row >= n_old && row < n_end) x[k] = *reinterpret_cast<const uint4*>(src);
+      src += src_step;
     }
+#pragma unroll
+    for (int k = 0; k < KV; ++k) mx = absmax8(mx, x[k]);
     mx = __reduce_max_sync(0xffffffffu, absmax_fold(mx));
     if constexpr (NT > 32) {
       if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = mx;
@@ -73,7 +77,7 @@ __global__ void __launch_bounds__(NT < 128 ? 128 : NT) append_q8_kernel(const Ap
     float s = q8_scale<TYPE>(mx), s_old = s;
     if (n_old > 0) s_old = *sp;
     // every thread has read the scale before it is written, and `red` before the
-    // next pair
+    // next group
     if constexpr (NT > 32)
       __syncthreads();
     else
@@ -96,9 +100,9 @@ __global__ void __launch_bounds__(NT < 128 ? 128 : NT) append_q8_kernel(const Ap
     const bool ok = s == s;
 #pragma unroll
     for (int k = 0; k < KV; ++k) {
-      const int i = lo + k * NT + tid;
-      if (i < hi)
-        *reinterpret_cast<uint2*>(dst + (long long)i * 8) =
+      const int row = row0 + k * step;
+      if (row >= n_old && row < n_end)
+        *reinterpret_cast<uint2*>(dst + (k * NT + tid) * 8) =
             ok ? q8_pack8<TYPE>(x[k], s, inv) : make_uint2(0, 0);
     }
     if (tid == 0) *sp = s;
@@ -216,8 +220,10 @@ template <int TYPE, int NT, int KV>
 static cudaError_t launch_append(const AppendQ8Args& a, cudaStream_t st) {
   constexpr int kCta = NT < 128 ? 128 : NT, kPer = kCta / NT;
   const int nb = ((a.n - 1) >> a.block_shift) + 2;  // blocks n rows may touch
-  const dim3 grid((nb + kPer - 1) / kPer, (unsigned)std::min(2 * a.Hkv * a.B, 65535));
-  return launch_k(append_q8_kernel<TYPE, NT, KV>, grid, dim3(kCta), 0, st, a);
+  AppendQ8Args args = a;
+  args.groups = (nb + kPer - 1) / kPer;
+  const dim3 grid((unsigned)(2 * a.Hkv * a.B), (unsigned)std::min(args.groups, 65535));
+  return launch_k(append_q8_kernel<TYPE, NT, KV>, grid, dim3(kCta), 0, st, args);
 }
 template <int TYPE>
 static cudaError_t launch_append_type(const AppendQ8Args& a, cudaStream_t st) {

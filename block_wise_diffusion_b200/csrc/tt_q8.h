@@ -24,6 +24,7 @@ inline cudaError_t allow_smem(size_t bytes) {
 struct AppendQ8Args {
   int B, Hkv, dh, L_cap, n, n_blocks;  // n_blocks: scales per (sequence, head)
   int block_shift;                     // 2^block_shift positions per scale
+  int groups;                          // of cache blocks that a CTA takes side by side
   const int* new_len;                         // optional [B]
   const uint16_t *k_new, *v_new;
   long long stride_b, stride_t, stride_h;     // elements

@@ -69,12 +69,6 @@ __device__ __forceinline__ uint32_t q8_exact(float x, float s, float t) {
 template <int TYPE>
 __device__ __forceinline__ uint2 q8_pack8(const uint4& v, float s, float inv) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  float t[8];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    t[2 * i] = __uint_as_float(w[i] << 16) * inv;
-    t[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u) * inv;
-  }
   uint2 r;
   bool rare;
   if constexpr (TYPE == TT_Q8_INT8) {
@@ -85,7 +79,7 @@ __device__ __forceinline__ uint2 q8_pack8(const uint4& v, float s, float inv) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float x = __uint_as_float(i & 1 ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16);
-      const float k = __fadd_rd(t[i], 12582912.f);
+      const float k = __fadd_rd(x * inv, 12582912.f);
       const float d = fmaf(-((k - 12582912.f) + 0.5f), s, x);
       m[i] = __float_as_uint(k) + 1u + (uint32_t)(__float_as_int(d) >> 31);
       tie = fminf(tie, fabsf(d));
@@ -94,39 +88,37 @@ __device__ __forceinline__ uint2 q8_pack8(const uint4& v, float s, float inv) {
     r = make_uint2(prmt(prmt(m[0], m[1], 0x40), prmt(m[2], m[3], 0x40), 0x5410),
                    prmt(prmt(m[4], m[5], 0x40), prmt(m[6], m[7], 0x40), 0x5410));
   } else {
-    // The conversion rounds t; that may be wrong only with the 20 bits below a
-    // normal's third fraction bit within 4 of 0x80000, or below 2^-6, where
-    // codes are 2^-9 apart.  Then the codes around t by its upper bits (below
-    // 2^-6: of t + 2^-6, whose spacing is theirs), up by one above the middle.
-    uint32_t d = 0xFFFFFFFFu;
-    float low = 1.f;
+    // The conversion rounds t; where t a little smaller and a little larger
+    // (2^-22 relative, more than its error) give the same code, x / s does too.
+    // Else, pair by pair, the codes around t by its upper bits (below 2^-6,
+    // where codes are 2^-9 apart: of t + 2^-6, whose spacing is theirs), up by
+    // one above the middle.
+    const float lo = inv * (1.f - 0x1p-22f), hi = inv * (1.f + 0x1p-22f);
+    uint32_t c[4];
+    float tie = 1.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      d = min(d, (__float_as_uint(t[i]) & 0xFFFFFu) - (0x80000u - 4u));
-      low = fminf(low, fabsf(t[i]));
-    }
-    r = make_uint2(cvt_e4m3x2(t[0], t[1]) | cvt_e4m3x2(t[2], t[3]) << 16,
-                   cvt_e4m3x2(t[4], t[5]) | cvt_e4m3x2(t[6], t[7]) << 16);
-    rare = false;
-    if (d <= 8u || low < 0.015625f) {
-      uint32_t c[8];
-      float tie = 1.f;
+    for (int i = 0; i < 4; ++i) {
+      const float x0 = __uint_as_float(w[i] << 16), x1 = __uint_as_float(w[i] & 0xFFFF0000u);
+      c[i] = cvt_e4m3x2(x0 * lo, x1 * lo);
+      if (c[i] != cvt_e4m3x2(x0 * hi, x1 * hi)) {
+        c[i] = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t xb = i & 1 ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16;
-        const bool sub = fabsf(t[i]) < 0.015625f;
-        const float o = sub ? 0.015625f : 0.f;
-        const uint32_t y = __float_as_uint(fabsf(t[i]) + o);
-        const float h = __uint_as_float((y & 0xFFF00000u) | 0x80000u) - o;
-        const float e = fmaf(-h, s, __uint_as_float(xb & 0x7FFFFFFFu));
-        c[i] = ((y >> 20) - (sub ? 968u : 960u) + 1u + (uint32_t)(__float_as_int(e) >> 31)) |
-               (xb >> 24 & 0x80u);
-        tie = fminf(tie, fabsf(e));
+        for (int k = 0; k < 2; ++k) {
+          const float x = k ? x1 : x0, u = fabsf(x * inv);
+          const bool sub = u < 0.015625f;
+          const float o = sub ? 0.015625f : 0.f;
+          const uint32_t y = __float_as_uint(u + o);
+          const float h = __uint_as_float((y & 0xFFF00000u) | 0x80000u) - o;
+          const float e = fmaf(-h, s, fabsf(x));
+          c[i] |= (((y >> 20) - (sub ? 968u : 960u) + 1u + (uint32_t)(__float_as_int(e) >> 31)) |
+                   (__float_as_uint(x) >> 24 & 0x80u))
+                  << (8 * k);
+          tie = fminf(tie, fabsf(e));
+        }
       }
-      rare = tie == 0.f;
-      r = make_uint2(prmt(prmt(c[0], c[1], 0x40), prmt(c[2], c[3], 0x40), 0x5410),
-                     prmt(prmt(c[4], c[5], 0x40), prmt(c[6], c[7], 0x40), 0x5410));
     }
+    rare = tie == 0.f;
+    r = make_uint2(prmt(c[0], c[1], 0x5410), prmt(c[2], c[3], 0x5410));
   }
   if (rare) {  // a true tie: to even
 #pragma unroll 1
