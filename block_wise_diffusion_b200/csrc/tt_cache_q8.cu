@@ -11,11 +11,12 @@ namespace tt {
 
 namespace {
 
-// A thread holds KV vectors of 8 values of one cache block, 8 of them except
-// in the smallest blocks, so a block of block * dh values takes 32 (16 x 64) to
-// 256 (128 x 128) threads.  A CTA has at least 128 threads, several blocks
-// side by side where they are small.
-constexpr int append_vectors(int block_values) { return block_values >= 2048 ? 8 : 4; }
+// A thread holds kVec vectors of 8 values of one cache block, so a block of
+// block * dh values takes 32 (16 x 64) to 512 (128 x 128) threads.  A CTA has at
+// least 128 threads, several blocks side by side where they are small.  (With
+// 8 vectors: 58 us against 56 for 16 prompts of up to 8192 tokens, the longer
+// code costing more than the shorter prologue saves.)
+constexpr int kVec = 4;
 
 // How many rows sequence b gets, or -1 when its lengths are out of range.
 __device__ __forceinline__ int append_rows(const AppendQ8Args& a, int b, int L) {
@@ -27,8 +28,8 @@ __device__ __forceinline__ int append_rows(const AppendQ8Args& a, int b, int L) 
 // sequence b's new rows may touch, counted from the block that holds its end,
 // y, y + gridDim.y, ..., so that neighbouring CTAs read neighbouring columns of
 // the same rows.  NT: threads of a block.
-template <int TYPE, int NT, int KV>
-__global__ void __launch_bounds__(NT < 128 ? 128 : NT, NT == 256 ? 4 : 8) append_q8_kernel(const AppendQ8Args a) {
+template <int TYPE, int NT>
+__global__ void __launch_bounds__(NT < 128 ? 128 : NT, NT == 512 ? 2 : NT == 256 ? 5 : 10) append_q8_kernel(const AppendQ8Args a) {
   constexpr int kCta = NT < 128 ? 128 : NT;
   griddep_launch();
   griddep_wait();
@@ -52,17 +53,17 @@ __global__ void __launch_bounds__(NT < 128 ? 128 : NT, NT == 256 ? 4 : 8) append
     const uint16_t* src = (is_v ? a.v_new : a.k_new) + (long long)b * a.stride_b +
                           (long long)g * a.stride_h + (p0 - L + row0) * a.stride_t + col * 8;
     const long long src_step = (long long)step * a.stride_t;
-    uint4 x[KV];
+    uint4 x[kVec];
     uint32_t mx = 0;
 #pragma unroll
-    for (int k = 0; k < KV; ++k) {
+    for (int k = 0; k < kVec; ++k) {
       const int row = row0 + k * step;
       x[k] = make_uint4(0, 0, 0, 0);
       if (row >= n_old && row < n_end) x[k] = *reinterpret_cast<const uint4*>(src);
       src += src_step;
     }
 #pragma unroll
-    for (int k = 0; k < KV; ++k) mx = absmax8(mx, x[k]);
+    for (int k = 0; k < kVec; ++k) mx = absmax8(mx, x[k]);
     mx = __reduce_max_sync(0xffffffffu, absmax_fold(mx));
     if constexpr (NT > 32) {
       if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = mx;
@@ -99,7 +100,7 @@ __global__ void __launch_bounds__(NT < 128 ? 128 : NT, NT == 256 ? 4 : 8) append
     const float inv = 1.f / s;
     const bool ok = s == s;
 #pragma unroll
-    for (int k = 0; k < KV; ++k) {
+    for (int k = 0; k < kVec; ++k) {
       const int row = row0 + k * step;
       if (row >= n_old && row < n_end)
         *reinterpret_cast<uint2*>(dst + (k * NT + tid) * 8) =
@@ -216,23 +217,23 @@ __global__ void __launch_bounds__(kQuantThreads)
 
 }  // namespace
 
-template <int TYPE, int NT, int KV>
+template <int TYPE, int NT>
 static cudaError_t launch_append(const AppendQ8Args& a, cudaStream_t st) {
   constexpr int kCta = NT < 128 ? 128 : NT, kPer = kCta / NT;
   const int nb = ((a.n - 1) >> a.block_shift) + 2;  // blocks n rows may touch
   AppendQ8Args args = a;
   args.groups = (nb + kPer - 1) / kPer;
   const dim3 grid((unsigned)(2 * a.Hkv * a.B), (unsigned)std::min(args.groups, 65535));
-  return launch_k(append_q8_kernel<TYPE, NT, KV>, grid, dim3(kCta), 0, st, args);
+  return launch_k(append_q8_kernel<TYPE, NT>, grid, dim3(kCta), 0, st, args);
 }
 template <int TYPE>
 static cudaError_t launch_append_type(const AppendQ8Args& a, cudaStream_t st) {
-  const int values = a.dh << a.block_shift, kv = append_vectors(values);
-  switch (values / (8 * kv)) {
-    case 32: return kv == 4 ? launch_append<TYPE, 32, 4>(a, st) : launch_append<TYPE, 32, 8>(a, st);
-    case 64: return launch_append<TYPE, 64, 8>(a, st);
-    case 128: return launch_append<TYPE, 128, 8>(a, st);
-    default: return launch_append<TYPE, 256, 8>(a, st);
+  switch ((a.dh << a.block_shift) / (8 * kVec)) {
+    case 32: return launch_append<TYPE, 32>(a, st);
+    case 64: return launch_append<TYPE, 64>(a, st);
+    case 128: return launch_append<TYPE, 128>(a, st);
+    case 256: return launch_append<TYPE, 256>(a, st);
+    default: return launch_append<TYPE, 512>(a, st);
   }
 }
 

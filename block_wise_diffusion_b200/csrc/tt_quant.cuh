@@ -94,31 +94,40 @@ __device__ __forceinline__ uint2 q8_pack8(const uint4& v, float s, float inv) {
     // where codes are 2^-9 apart: of t + 2^-6, whose spacing is theirs), up by
     // one above the middle.
     const float lo = inv * (1.f - 0x1p-22f), hi = inv * (1.f + 0x1p-22f);
-    uint32_t c[4];
+    uint32_t c[4], open = 0;
     float tie = 1.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float x0 = __uint_as_float(w[i] << 16), x1 = __uint_as_float(w[i] & 0xFFFF0000u);
       c[i] = cvt_e4m3x2(x0 * lo, x1 * lo);
-      if (c[i] != cvt_e4m3x2(x0 * hi, x1 * hi)) {
-        c[i] = 0;
+      open |= c[i] != cvt_e4m3x2(x0 * hi, x1 * hi) ? 1u << i : 0u;
+    }
+    r = make_uint2(prmt(c[0], c[1], 0x5410), prmt(c[2], c[3], 0x5410));
+    // (a loop, not four copies: code that few lanes run should not fill the
+    // instruction cache)
+#pragma unroll 1
+    for (; open != 0; open &= open - 1) {
+      const int i = __ffs(open) - 1;
+      const uint32_t wi = i < 2 ? (i ? v.y : v.x) : (i == 2 ? v.z : v.w);
+      uint32_t code = 0;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const float x = k ? x1 : x0, u = fabsf(x * inv);
-          const bool sub = u < 0.015625f;
-          const float o = sub ? 0.015625f : 0.f;
-          const uint32_t y = __float_as_uint(u + o);
-          const float h = __uint_as_float((y & 0xFFF00000u) | 0x80000u) - o;
-          const float e = fmaf(-h, s, fabsf(x));
-          c[i] |= (((y >> 20) - (sub ? 968u : 960u) + 1u + (uint32_t)(__float_as_int(e) >> 31)) |
-                   (__float_as_uint(x) >> 24 & 0x80u))
-                  << (8 * k);
-          tie = fminf(tie, fabsf(e));
-        }
+      for (int k = 0; k < 2; ++k) {
+        const float x = __uint_as_float(k ? wi & 0xFFFF0000u : wi << 16), u = fabsf(x * inv);
+        const bool sub = u < 0.015625f;
+        const float o = sub ? 0.015625f : 0.f;
+        const uint32_t y = __float_as_uint(u + o);
+        const float h = __uint_as_float((y & 0xFFF00000u) | 0x80000u) - o;
+        const float e = fmaf(-h, s, fabsf(x));
+        code |= (((y >> 20) - (sub ? 968u : 960u) + 1u + (uint32_t)(__float_as_int(e) >> 31)) |
+                 (__float_as_uint(x) >> 24 & 0x80u))
+                << (8 * k);
+        tie = fminf(tie, fabsf(e));
       }
+      const uint32_t sel = i & 1 ? 0x5410u : 0x3254u;
+      uint32_t& half = i < 2 ? r.x : r.y;
+      half = prmt(half, code, sel);
     }
     rare = tie == 0.f;
-    r = make_uint2(prmt(c[0], c[1], 0x5410), prmt(c[2], c[3], 0x5410));
   }
   if (rare) {  // a true tie: to even
 #pragma unroll 1
