@@ -253,6 +253,7 @@ tt_status tt_block_denoise_attn_q8(const tt_dims* d, const tt_q8* f, const tt_bf
   a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)d->dh));
   a.out = out;
   a.s_per_half = g.s_per_half;
+  while ((1 << a.g_shift) < g.G) ++a.g_shift;
   a.rows_per_half = g.rows_per_half;
   a.halves = g.halves;
   a.n_qtiles = g.n_qtiles;

@@ -45,7 +45,6 @@ constexpr int kConv = 128;                  // converter threads
 constexpr int kSlots = 2;                   // depth of the K and of the V ring
 constexpr uint32_t kSub = kAttnBN * 128;    // 128 rows x 64 fp16: 16 KB
 constexpr float kRescale = 8.0f;            // log2 units the running maximum may lag
-constexpr int kL2Ahead = 3;                 // tiles brought into L2 ahead of their load
 
 struct Smem {
   uint32_t q, k, v, raw, scales, bars, total;
@@ -285,29 +284,47 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
       const size_t slot = (size_t)ub * U + uk + blockIdx.x;
       const int step = split ? 2 : 1, first = sa + (split ? ch : 0);
       float m = -INFINITY, l = 0.f;
-      const int s_pos = qt * a.halves * a.s_per_half + (split ? 0 : ch * a.s_per_half) + r / a.G;
-      const size_t qrow = ((size_t)ub * a.S + s_pos) * a.Hq + ug * a.G + r % a.G;
+      // block positions (times heads) of the chain's rows
+      const size_t pos0 =
+          (size_t)ub * a.S + qt * a.halves * a.s_per_half + (split ? 0 : ch * a.s_per_half);
+      const size_t qrow = (pos0 + (r >> a.g_shift)) * a.Hq + ug * a.G + (r & (a.G - 1));
       if (first < sb) {
-        // The query row, by a power of two in fp16 range.  The previous
+        // The warp's 32 query rows, each by a power of two in fp16 range: a row
+        // to DH / 8 lanes, so that loads are whole lines (a row to a thread
+        // took 8,000 cycles, these 2,000), eight in flight.  The previous
         // segment's last S of this chain has been waited for below.
         float c_row = 0.f;
         {
-          const uint4 zero = make_uint4(0, 0, 0, 0);
-          // all of the row's loads in flight at once
-          const uint4* src = reinterpret_cast<const uint4*>(a.q + qrow * DH);
-          uint4 x[DH / 8];
-          uint32_t mx = 0;
+          constexpr int LPR = DH / 8, RPL = 32 / LPR;  // lanes per row, rows per load
+          const int rl = lane / LPR, cl = lane % LPR;
+          const int r0 = (warp & 3) * 32;
+#pragma unroll 1
+          for (int i0 = 0; i0 < LPR; i0 += 8) {
+            uint4 x[8];
 #pragma unroll
-          for (int i = 0; i < DH / 8; ++i) x[i] = valid ? src[i] : zero;
+            for (int i = 0; i < 8; ++i) {
+              const int rr = r0 + (i0 + i) * RPL + rl;
+              x[i] = make_uint4(0, 0, 0, 0);
+              if (rr < a.rows_per_half)
+                x[i] = *reinterpret_cast<const uint4*>(
+                    a.q + ((size_t)(pos0 + (rr >> a.g_shift)) * a.Hq + ug * a.G + (rr & (a.G - 1))) * DH +
+                    cl * 8);
+            }
 #pragma unroll
-          for (int i = 0; i < DH / 8; ++i) mx = absmax_bf16x8(mx, x[i]);
-          const int e = norm_exp(max(mx & 0xFFFFu, mx >> 16));
-          const float f = pow2i(-e);
-          c_row = a.scale_log2 * pow2i(e);
+            for (int i = 0; i < 8; ++i) {
+              const int rr = r0 + (i0 + i) * RPL + rl;
+              uint32_t mx = absmax_bf16x8(0, x[i]);
+              mx = max(mx & 0xFFFFu, mx >> 16);
 #pragma unroll
-          for (int i = 0; i < DH / 8; ++i)
-            sts128(sQ + chunk_at(r, i), bf16x2_to_f16x2(x[i].x, f), bf16x2_to_f16x2(x[i].y, f),
-                   bf16x2_to_f16x2(x[i].z, f), bf16x2_to_f16x2(x[i].w, f));
+              for (int o = LPR / 2; o > 0; o >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+              const int e = norm_exp(mx);
+              const float f = pow2i(-e);
+              sts128(sQ + chunk_at(rr, cl), bf16x2_to_f16x2(x[i].x, f), bf16x2_to_f16x2(x[i].y, f),
+                     bf16x2_to_f16x2(x[i].z, f), bf16x2_to_f16x2(x[i].w, f));
+              const int mine = __shfl_sync(0xffffffffu, e, (lane % RPL) * LPR);
+              if (lane / RPL == i0 + i) c_row = a.scale_log2 * pow2i(mine);
+            }
+          }
         }
         fence_proxy_async_smem();
         mbar_arrive(&q_full[ch]);
@@ -574,7 +591,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
     if (warp == 14) {
       // ----------------------------------------- codes to shared memory
       // One K and one V tile of codes (contiguous in memory) ahead of the
-      // converters, and kL2Ahead tiles brought into L2 before that.
+      // converters.  (Tiles further ahead brought into L2 cost more, in the
+      // first tiles, than they saved.)
       if (lane == 0) {
         const uint32_t rK = smem_u32(base + SL.raw), rV = rK + kAttnBN * DH;
         int raw = 0;
@@ -583,17 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
           const size_t pair = (size_t)ub * a.Hkv + uk / a.n_qtiles;
           const uint8_t* kp = a.k_ctx + pair * a.L_cap * DH;
           const uint8_t* vp = a.v_ctx + pair * a.L_cap * DH;
-          auto ahead = [&](int tl) {
-            if (tl > 0 && tl < sb) {
-              const size_t at = (size_t)(tl - 1) * kAttnBN * DH;
-              const uint32_t n = (uint32_t)tile_keys(tl, L, a.S) * DH;
-              prefetch_l2_bulk(kp + at, n);
-              prefetch_l2_bulk(vp + at, n);
-            }
-          };
-          for (int k = 1; k < kL2Ahead; ++k) ahead(sa + k);
           for (int tl = sa; tl < sb; ++tl) {
-            ahead(tl + kL2Ahead);
             if (tl == 0) continue;
             const size_t at = (size_t)(tl - 1) * kAttnBN * DH;
             const uint32_t n = (uint32_t)tile_keys(tl, L, a.S) * DH;

@@ -19,14 +19,15 @@ namespace tt {
 // One position in the tile sequence and what is left of the CTA's range.
 struct TileWalk {
   const int* ctx_len;
-  int left;      // tiles of the range not yet handed out
-  int L_cap, U;  // units per sequence
-  int b, k;      // sequence, unit within it
-  int off;       // tile within the unit
+  int left;         // tiles of the range not yet handed out
+  int B, L_cap, U;  // U: units per sequence
+  int b, k;         // sequence, unit within it
+  int off;          // tile within the unit
+  int len;          // sequence b's context length, loaded when b is reached
   // The next segment: unit (b, k), local tiles [a, e), context length L.
   __device__ __forceinline__ bool next(int& sb, int& sk, int& a, int& e, int& L) {
     if (left <= 0) return false;
-    L = min(max(ctx_len[b], 0), L_cap);
+    L = min(max(len, 0), L_cap);
     const int n = 1 + (L + kAttnBN - 1) / kAttnBN;
     sb = b;
     sk = k;
@@ -37,6 +38,7 @@ struct TileWalk {
     if (++k == U) {
       k = 0;
       ++b;
+      len = b < B ? ctx_len[b] : 0;
     }
     return true;
   }
@@ -99,12 +101,13 @@ __device__ __forceinline__ TileWalk plan_walk(const AttnQ8Args& a, PlanSmem& sm)
   __syncthreads();
   TileWalk w;
   w.ctx_len = a.ctx_len;
+  w.B = a.B;
   w.L_cap = a.L_cap;
   w.U = U;
   w.left = cta_first(blockIdx.x + 1, T, a.n_ctas) - lo;
   w.b = sm.b;
-  int x = 0;
-  const int n = tiles(w.b, x);
+  w.len = a.ctx_len[w.b];
+  const int n = 1 + (min(max(w.len, 0), a.L_cap) + kAttnBN - 1) / kAttnBN;
   const int rem = lo - sm.pre * U;
   w.k = rem / n;
   w.off = rem - w.k * n;

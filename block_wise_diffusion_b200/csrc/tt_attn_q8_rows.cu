@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_rows_kernel(const AttnQ8A
 
     // the next unit's first keys to L2, while this one's results are joined
     if (threadIdx.x < 2 && walk.left > 0) {
-      const int nL = min(max(a.ctx_len[walk.b], 0), a.L_cap);
+      const int nL = min(max(walk.len, 0), a.L_cap);
       const int nk = min(min(nL, (walk.left - 1) * kAttnBN), kWarps * kGroup);
       if (nk > 0)
         prefetch_l2_bulk((threadIdx.x ? a.v_ctx : a.k_ctx) +

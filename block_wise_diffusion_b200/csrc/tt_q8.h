@@ -90,6 +90,7 @@ struct AttnQ8Args {
   float scale_log2;  // log2(e) / sqrt(dh)
   uint16_t* out;
   int s_per_half, rows_per_half, halves, n_qtiles, units, n_ctas;
+  int g_shift;      // G = 2^g_shift
   int2* unit_span;  // [units] first and last CTA that hold tiles of the unit
   float* part_o;   // [units + n_ctas - 1] unnormalised outputs of segments:
                    // [dh/4][256 rows][4], or [16 rows][dh] (at most 16 rows)
