@@ -24,7 +24,10 @@
 // 128 columns hold a P of its own for each chain, and the next S does not
 // wait for this tile's softmax and P . V: with S and P in the same columns
 // (two S buffers) every tile paid S, softmax and P . V one after the other,
-// 4,900 cycles for the two chains where this order takes @@.
+// 4,900 cycles for the two chains where this order takes 3,500 to 3,900.
+// The block's own keys are a unit's last tile: their conversion from bf16 (two
+// passes, 13,000 cycles when nothing hides them) then runs under the softmax of
+// the tiles before (48 sequences of up to 32768 keys: 219 us; as first tile 239).
 // Roles (16 warps; registers are moved to the softmax by setmaxnreg):
 //   warps 0-3 / 4-7   softmax of chain 0 / 1;
 //   warps 8-11        codes of one tile in shared memory to fp16 in the swizzled
@@ -69,6 +72,12 @@ __device__ __forceinline__ uint8_t* align1024(uint8_t* p) {
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn_major) {
   return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) |
          ((uint32_t)(M >> 4) << 24);
+}
+
+// Valid keys of local tile t: 128 context keys each, then the block's own S keys.
+__device__ __forceinline__ bool is_context(int t, int L) { return t * kAttnBN < L; }
+__device__ __forceinline__ int tile_keys(int t, int L, int S) {
+  return is_context(t, L) ? min(kAttnBN, L - t * kAttnBN) : S;
 }
 
 // Pairs of fp32 in one 64-bit register: one instruction for two.
@@ -291,7 +300,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
       if (first < sb) {
         // The warp's 32 query rows, each by a power of two in fp16 range: a row
         // to DH / 8 lanes, so that loads are whole lines (a row to a thread
-        // took 8,000 cycles, these 2,000), eight in flight.  The previous
+        // took 8,000 cycles, these 2,000), eight in flight: all sixteen of dh 128
+        // at once unroll to more instructions than they save (+7 % on long caches).  The previous
         // segment's last S of this chain has been waited for below.
         float c_row = 0.f;
         {
@@ -557,10 +567,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
         const int slot = split ? (tl - sa) & 1 : kt & 1;
         const uint32_t par = ((uint32_t)(slot ? used1++ : used0++) & 1u) ^ 1u;
         const int nv = tile_keys(tl, L, a.S);
-        int ek = 0;
+        const bool ctx = is_context(tl, L);
+        int ek = 0;  // exponent of the block's K rows
 #pragma unroll 1
         for (int kv = 0; kv < 2; ++kv) {  // K, then V
-          if ((tl > 0 && !mbar_wait_inline(&rk_full[kv], (uint32_t)raw & 1u, a.err, abort_flag,
+          if ((ctx && !mbar_wait_inline(&rk_full[kv], (uint32_t)raw & 1u, a.err, abort_flag,
                                            WHERE_ATTN_PRODUCER)) ||
               !mbar_wait_inline(&empty[2 * kv + slot], par, a.err, abort_flag,
                                 WHERE_ATTN_PRODUCER)) {
@@ -568,7 +579,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
             break;
           }
           const uint32_t dst = sK + (kv * kSlots + slot) * NSUB * kSub;
-          if (tl == 0) {
+          if (!ctx) {
             const int e = block_rows((kv ? a.v_blk : a.k_blk) +
                                          ((size_t)ub * a.S * a.Hkv + ug) * DH, dst, kv);
             // the block's scales; V's slot, once free, frees the scales' too
@@ -602,8 +613,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
           const uint8_t* kp = a.k_ctx + pair * a.L_cap * DH;
           const uint8_t* vp = a.v_ctx + pair * a.L_cap * DH;
           for (int tl = sa; tl < sb; ++tl) {
-            if (tl == 0) continue;
-            const size_t at = (size_t)(tl - 1) * kAttnBN * DH;
+            if (!is_context(tl, L)) break;  // the unit's last tile
+            const size_t at = (size_t)tl * kAttnBN * DH;
             const uint32_t n = (uint32_t)tile_keys(tl, L, a.S) * DH;
             const uint32_t par = ((uint32_t)raw & 1u) ^ 1u;
             ok = mbar_wait_inline(&rk_empty[0], par, a.err, abort_flag, WHERE_ATTN_PRODUCER);
@@ -630,8 +641,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
         const float* vsp = a.v_scale + pair * a.n_blocks;
         float nk = 1.f, nw = 1.f;  // a tile ahead
         auto load = [&](int tl) {
-          const int pos = (tl - 1) * kAttnBN + lane * 16;
-          const bool in = lane < 8 && tl > 0 && tl < sb && pos < L;
+          const int pos = tl * kAttnBN + lane * 16;
+          const bool in = lane < 8 && tl < sb && pos < L;
           nk = in ? __ldg(ksp + (pos >> a.block_shift)) : 1.f;
           nw = in ? __ldg(vsp + (pos >> a.block_shift)) : 1.f;
         };
@@ -641,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
           const uint32_t par = ((uint32_t)(slot ? used1++ : used0++) & 1u) ^ 1u;
           ok = mbar_wait_inline(&empty[2 + slot], par, a.err, abort_flag, WHERE_ATTN_PRODUCER);
           if (!ok) break;
-          if (tl > 0 && lane < 8)
+          if (is_context(tl, L) && lane < 8)
             put_scales(scales + slot * 24, lane, nk, log2f(nw), 1.f / nw, &sc_full[slot]);
           load(tl + 1);
           __syncwarp();

@@ -2,8 +2,8 @@
 // the exact handling of ranges.
 //
 // Schedule.  A unit is (sequence, KV head, query tile); all units of a
-// sequence have the same number of key tiles (tile 0: the block's own keys,
-// then 128 context keys each), so the tile sequence is described by prefix
+// sequence have the same number of key tiles (one with the block's own keys, the
+// others with 128 context keys each), so the tile sequence is described by prefix
 // sums over the B sequences alone, and every CTA computes them itself from
 // ctx_len instead of waiting for a planning kernel.  CTA c takes the tiles
 // [c T / P, (c + 1) T / P) of the T tiles; its part of unit u (a segment) has
@@ -112,11 +112,6 @@ __device__ __forceinline__ TileWalk plan_walk(const AttnQ8Args& a, PlanSmem& sm)
   w.k = rem / n;
   w.off = rem - w.k * n;
   return w;
-}
-
-// Valid keys of local tile t (0: the block's own keys).
-__device__ __forceinline__ int tile_keys(int t, int L, int S) {
-  return t == 0 ? S : min(kAttnBN, L - (t - 1) * kAttnBN);
 }
 
 // Recorded for the merge by the CTAs that hold a unit's first and last tile: all
