@@ -453,7 +453,7 @@ def _arg(x, name: str, nbytes: int, dev: int) -> int | None:
 
 def _raw_stream(stream, dev: int) -> int | None:
     if stream is None:
-        return _torch._C._cuda_getCurrentRawStream(dev)
+        return _torch._C._cuda_getCurrentRawStream(dev) if dev >= 0 else _stream(None)
     return stream if type(stream) is int else stream.cuda_stream
 
 

@@ -50,6 +50,14 @@ tt_status check_fmt(const tt_q8* f) {
   return TT_OK;
 }
 
+// Positions rounded up to a whole tile or block stay in 32 bits.
+tt_status check_cache(const tt_dims* d, const tt_q8* f) {
+  Q8_CHECK(check_dims_public(d));
+  Q8_CHECK(check_fmt(f));
+  if (d->L_cap > 0x7fffff00) return set_errorf(TT_ERR_UNSUPPORTED, "L_cap=%d too large", d->L_cap);
+  return TT_OK;
+}
+
 int block_shift(const tt_q8& f) { return f.block == 16 ? 4 : f.block == 32 ? 5 : f.block == 64 ? 6 : 7; }
 
 tt_status check_ws_ptr(void* ws, size_t have, size_t need) {
@@ -212,8 +220,7 @@ tt_status tt_block_denoise_attn_q8(const tt_dims* d, const tt_q8* f, const tt_bf
                                    const void* v_ctx, const float* k_scale, const float* v_scale,
                                    const int32_t* ctx_len, tt_bf16* out, void* ws,
                                    size_t ws_bytes, void* stream) {
-  Q8_CHECK(check_dims_public(d));
-  Q8_CHECK(check_fmt(f));
+  Q8_CHECK(check_cache(d, f));
   Q8_CHECK(check_ptr(q_blk, "q_blk", 16));
   Q8_CHECK(check_ptr(k_blk, "k_blk", 16));
   Q8_CHECK(check_ptr(v_blk, "v_blk", 16));
@@ -278,8 +285,7 @@ tt_status tt_append_ctx_q8(const tt_dims* d, const tt_q8* f, int32_t n, const in
                            const tt_row_strides* strides, void* k_ctx, void* v_ctx,
                            float* k_scale, float* v_scale, int32_t* ctx_len, void* ws,
                            size_t ws_bytes, void* stream) {
-  Q8_CHECK(check_dims_public(d));
-  Q8_CHECK(check_fmt(f));
+  Q8_CHECK(check_cache(d, f));
   if (n < 1 || n > d->L_cap)
     return set_errorf(TT_ERR_INVALID_ARG, "n=%d not in [1, L_cap=%d]", n, d->L_cap);
   if (strides == nullptr) return set_errorf(TT_ERR_INVALID_ARG, "strides is NULL");

@@ -65,6 +65,15 @@ def test_attention_pointers(L, i, name, align):
     assert attn(L, _d(), tt.q8("int8", 64), p) == 1 and "aligned" in tt.tt_last_error()
 
 
+def test_longest_context(L):
+    """Lengths are rounded up to whole tiles in 32 bits."""
+    d, st = _d(B=1, Hq=2, dh=64, L_cap=(1 << 31) - 1), (64, 64, 64)
+    d.Hkv, d.Hq, d.H = 1, 1, 64
+    for f in (tt.q8("int8", 16), tt.q8("e4m3", 128)):
+        assert attn(L, d, f) == 2 and "L_cap" in tt.tt_last_error()
+        assert append(L, d=d, f=f, st=st) == 2 and "L_cap" in tt.tt_last_error()
+
+
 def test_attention_workspace(L):
     need = tt.tt_workspace_bytes(_d(), tt.TT_WS_ATTN_Q8)
     assert attn(L, _d(), tt.q8("int8", 64), ws_bytes=need - 1) == 3
