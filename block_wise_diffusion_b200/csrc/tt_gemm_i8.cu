@@ -314,9 +314,11 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
-                   : "memory");
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // 16 bytes to the same shared-memory address of CTA `rank` of the cluster.
 __device__ __forceinline__ void st_cluster(uint32_t saddr, uint32_t rank, uint32_t x, uint32_t y,
@@ -372,6 +374,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  if (splits > 1) cluster_arrive();  // this CTA runs: its memory may be written
 
   if (warp == 0) {
     if (lane == 0) {
@@ -430,6 +433,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   const int q = warp & 3, row128 = q * 32 + lane;
   const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16);
   const int part = BN / splits;  // columns this CTA finishes: rank * part ..
+  __syncwarp();
+  if (splits > 1) cluster_wait();  // all CTAs of the cluster run
   bool ok = warp >= 2 && mbar_wait(accf, 0, a.err, abort_flag, WHERE_GEMM_EPI);
   if (ok) tc_fence_after();
   if (ok && splits > 1) {
@@ -458,7 +463,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   // every thread of the cluster arrives, whatever happened above
   if (splits > 1) {
     __syncthreads();
-    cluster_sync();
+    cluster_arrive();
+    cluster_wait();
   }
   if (ok) {
     griddep_wait();  // the rows' scales
