@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         // Per row: the maximum of sum * column scale, the sum of exponentials
         // relative to it (differences first, so large logits lose nothing),
         // and the lowest column that attains it.
-        const float c = a.scale_log2 * rs;
+        const float c = row_factor(a.scale_log2, rs);
         float best = -INFINITY, z = 0.f;
         int bidx = 0;
         for (int ch = 0; ch < nchunks; ++ch) {

@@ -292,6 +292,14 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// scale_log2 times a row's factor, kept finite and above zero (NaN stays NaN):
+// a difference of logits times it is 0 or less, also where one is infinite.
+// The smallest denormal stands for anything below: no difference of two fp32
+// numbers times that reaches 2^-20.
+__device__ __forceinline__ float row_factor(float scale_log2, float row) {
+  const float c = scale_log2 * row;
+  return c != c ? c : fminf(fmaxf(c, 1.401298464e-45f), 3.402823466e38f);
+}
 // float -> bf16 bits (round to nearest even) and back
 __device__ __forceinline__ uint16_t bf16_bits(float x) {
   uint16_t r;

@@ -495,8 +495,9 @@ __global__ void __launch_bounds__(kCommitThreads) commit_kernel(const CommitArgs
   const int M = a.M_dev != nullptr ? *a.M_dev : a.B * S;
   if (a.masked[row] != 0) {
     const int j = a.rowlist[a.B * S + row];  // this row's compact index
-    const float c =
-        a.scale_log2 * (a.row_scale != nullptr && j >= 0 && j < M ? a.row_scale[j] : 1.f);
+    const float c = a.row_scale != nullptr && j >= 0 && j < M
+                        ? row_factor(a.scale_log2, a.row_scale[j])
+                        : a.scale_log2;
     RowBest rb{-INFINITY, 0.f, 0x7fffffff, -1};
     if (j >= 0 && j < M) {
       // thread i reads tiles i, i + kCommitThreads, ...: all loads first

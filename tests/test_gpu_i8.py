@@ -245,6 +245,22 @@ def test_vocab_zero_and_non_finite_rows():
         np.testing.assert_array_equal(bad[k][0], got[k][0])
 
 
+def test_vocab_extreme_logit_scales():
+    """A row's factor that underflows makes every logit equal, one that overflows
+    leaves the largest alone; neither is a NaN."""
+    y = np.random.default_rng(12).standard_normal((16, 128))
+    y[3] = 0.0                                       # scale 2^-60
+    got, ref, tokens, m = vocab(1, 16, 128, 300, 0.9, 1e-35, 12, y=y)
+    assert got["status"] == 0
+    np.testing.assert_allclose(got["conf"], 1 / 300, rtol=2.0 ** -18)
+    got, ref, tokens, m = vocab(1, 16, 128, 300, 0.9, 3e38, 12, y=y * 2.0 ** 9)
+    assert got["status"] == 0
+    sure = ref["sure"].copy()
+    sure[0, 3] = False
+    assert sure.sum() > 12 and (got["conf"][sure] == 1).all()
+    np.testing.assert_array_equal(got["tok"][sure], ref["tok"][sure])
+
+
 def test_vocab_captured_twice_on_their_own_workspaces():
     rng = np.random.default_rng(11)
     B, S, Hh, V = 3, 16, 256, 3000
