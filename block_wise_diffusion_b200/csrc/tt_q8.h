@@ -55,7 +55,7 @@ cudaError_t launch_masked_rows(const uint16_t* x, int K, int8_t* q, float* scale
 // per tile.
 constexpr int kI8BM = 128, kI8BK = 128;
 constexpr int kI8VocabBN = kVocabBN, kI8VocabStages = 5;
-constexpr int kI8BN = 256, kI8Stages = 4;
+constexpr int kI8BN = 256, kI8Stages = 4, kI8PairStages = 6;
 struct GemmI8Args {
   int M_alloc;           // rows of A
   int a_box;             // rows of a TMA box of A: fewer than 128 when A has fewer (the
@@ -71,8 +71,10 @@ struct GemmI8Args {
 };
 cudaError_t launch_gemm_i8_vocab(const CUtensorMap& tmA, const CUtensorMap& tmB,
                                  const GemmI8Args& a, int grid, cudaStream_t st);
+// grid: CTAs, or pairs of CTAs with `pair` (256-row tiles; tmB's box then has half
+// a tile's columns).
 cudaError_t launch_gemm_i8_linear(const CUtensorMap& tmA, const CUtensorMap& tmB,
-                                  const GemmI8Args& a, int grid, cudaStream_t st);
+                                  const GemmI8Args& a, bool pair, int grid, cudaStream_t st);
 // Few tiles: `splits` CTAs (a power of two, at most bn / 16) to a 128 x bn tile,
 // bn 32, 64 or 128.
 cudaError_t launch_gemm_i8_split(const CUtensorMap& tmA, const CUtensorMap& tmB,
