@@ -149,8 +149,8 @@ LinearWs carve_linear(int rows, int K, void* ws) {
 // 128 columns are no more than the SMs, each tile goes to a cluster of `splits`
 // CTAs that share its K: of the shapes that fit, the one whose CTAs read the
 // fewest bytes, an exchange of partial sums counted as 200 KB (about 1 us).
-// 128 x 4608, K = 4096: 72 tiles of 64 in pairs 11.2 us, 144 of 32 alone 12.8,
-// 36 of 128 in fours 17.3 (clusters of four leave SMs of a GPC over, so not
+// 128 x 4608, K = 4096: 72 tiles of 64 in pairs 11.5 us, 144 of 32 alone 12.6,
+// 36 of 128 in fours 16.8 (clusters of four leave SMs of a GPC over, so not
 // all 36 run at once: more than two CTAs only within 7/8 of the SMs).
 // splits = 0: more tiles than SMs; 256-wide tiles, one CTA each in turn, which
 // read A less often.

@@ -18,6 +18,9 @@
 // of its own (the formulas of tt_attn_q8.cu) and refills a register buffer as
 // soon as the products have read it.  The 8 warps' results are joined through
 // shared memory at a segment's end.
+// What bounds it: the instructions per key, most of them the codes' conversion.
+// 64 sequences of up to 8192 keys, 2 KV heads of 16 queries, dh 128, with the
+// merge: e4m3 46 us (3.0 TB/s), int8, whose conversion is longer, 49.
 #include <math.h>
 
 #include "tt_attn_q8.cuh"
