@@ -94,15 +94,20 @@ __device__ __forceinline__ uint2 q8_pack8(const uint4& v, float s, float inv) {
     // where codes are 2^-9 apart: of t + 2^-6, whose spacing is theirs), up by
     // one above the middle.
     const float lo = inv * (1.f - 0x1p-22f), hi = inv * (1.f + 0x1p-22f);
-    uint32_t c[4], open = 0;
+    uint32_t c[4], d[4];
     float tie = 1.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float x0 = __uint_as_float(w[i] << 16), x1 = __uint_as_float(w[i] & 0xFFFF0000u);
       c[i] = cvt_e4m3x2(x0 * lo, x1 * lo);
-      open |= c[i] != cvt_e4m3x2(x0 * hi, x1 * hi) ? 1u << i : 0u;
+      d[i] = cvt_e4m3x2(x0 * hi, x1 * hi);
     }
     r = make_uint2(prmt(c[0], c[1], 0x5410), prmt(c[2], c[3], 0x5410));
+    const uint32_t dx = r.x ^ prmt(d[0], d[1], 0x5410), dy = r.y ^ prmt(d[2], d[3], 0x5410);
+    uint32_t open = 0;
+    if ((dx | dy) != 0)
+      open = ((dx & 0xFFFFu) != 0) | ((dx >> 16) != 0) << 1 | ((dy & 0xFFFFu) != 0) << 2 |
+             ((dy >> 16) != 0) << 3;
     // (a loop, not four copies: code that few lanes run should not fill the
     // instruction cache)
 #pragma unroll 1

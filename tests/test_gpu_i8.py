@@ -57,7 +57,8 @@ def linear(rows, N, K, seed, extreme=False):
     (1, 1, 16), (1, 8, 64), (16, 384, 256), (17, 389, 112), (128, 4608, 1024), (129, 257, 4096),
     (300, 1000, 2000), (5, 4608, 4096), (1, 9000, 4096), (64, 513, 8192), (2000, 72, 320), (3, 24, 131072),
     (257, 1024, 144), (128, 128, 16384),
-    (300, 13001, 144), (257, 26000, 2064), (2100, 2600, 256), (1025, 6400, 128)])
+    (300, 13001, 144), (257, 26000, 2064), (2100, 2600, 256), (1025, 6400, 128),
+    (40000, 24, 64), (20000, 1, 16)])
 def test_linear_matches_oracle(rows, N, K):
     linear(rows, N, K, rows + N + K)
 
