@@ -8,8 +8,9 @@
 // x - h s decides: h has a short significand, so one FMA rounds that
 // difference without losing its sign, and 0 is a true tie.
 // Such quotients are no rarity: half a group's largest value always lies within
-// a rounding of a middle of int8 codes (63.5), one value in a thousand of
-// normal data.  So nothing here takes a long path for them.
+// a rounding of a middle of int8 codes (63.5), and one value in 200 of normal
+// data is that near to one of e4m3, half of them on it, which a third of a warp's
+// vectors meet.  So nothing here takes a long path for them.
 #pragma once
 #include <stdint.h>
 
@@ -30,17 +31,6 @@ __device__ __forceinline__ float q8_scale(uint32_t amax) {
   return fmaxf(__fmul_rn(bf16_value((uint16_t)amax), kInv), kScaleFloor);
 }
 
-// Nearest of a grid of spacing `step` (a power of two) to y / s, ties to even
-// multiples, given t within 2^-22 relative of y / s; y, s > 0.
-__device__ __forceinline__ float round_exact(float y, float s, float t, float step) {
-  const float k2 = rintf(2.f * t / step);  // in half steps (exact scaling)
-  const float lo = floorf(0.5f * k2);      // grid index at or below
-  if (k2 == 2.f * lo) return lo * step;    // nearer to a grid point than to a middle
-  const float r = fmaf(-(lo + 0.5f) * step, s, y);
-  const float even = 2.f * rintf(0.5f * lo) == lo ? lo : lo + 1.f;
-  return (r > 0.f ? lo + 1.f : r < 0.f ? lo : even) * step;
-}
-
 __device__ __forceinline__ uint32_t cvt_e4m3x2(float lo, float hi) {
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
@@ -50,27 +40,11 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
   return __byte_perm(a, b, sel);
 }
 
-// The exact code of one value as a byte.
-template <int TYPE>
-__device__ __forceinline__ uint32_t q8_exact(float x, float s, float t) {
-  if constexpr (TYPE == TT_Q8_INT8) {
-    const float n = round_exact(fabsf(x), s, fabsf(t), 1.f);
-    return (uint32_t)(int)copysignf(fminf(n, 127.f), x) & 255u;
-  } else {
-    // codes are 2^(e - 3) apart, e the quotient's exponent, at least -6
-    const uint32_t u = __float_as_uint(t) & 0x7FFFFFFFu;
-    const int e = max((int)(u >> 23) - 127, -6);
-    const float step = __uint_as_float((uint32_t)(e - 3 + 127) << 23);
-    return cvt_e4m3x2(copysignf(round_exact(fabsf(x), s, fabsf(t), step), x), 0.f) & 255u;
-  }
-}
-
 // Eight bf16 values (one 16-byte vector) to eight codes; inv = 1 / s.
 template <int TYPE>
 __device__ __forceinline__ uint2 q8_pack8(const uint4& v, float s, float inv) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
   uint2 r;
-  bool rare;
   if constexpr (TYPE == TT_Q8_INT8) {
     // Rounded down by adding 1.5 * 2^23 (the integer's two's complement is then
     // in the low byte), and up by one where x lies above the middle.
@@ -84,18 +58,29 @@ __device__ __forceinline__ uint2 q8_pack8(const uint4& v, float s, float inv) {
       m[i] = __float_as_uint(k) + 1u + (uint32_t)(__float_as_int(d) >> 31);
       tie = fminf(tie, fabsf(d));
     }
-    rare = tie == 0.f;
     r = make_uint2(prmt(prmt(m[0], m[1], 0x40), prmt(m[2], m[3], 0x40), 0x5410),
                    prmt(prmt(m[4], m[5], 0x40), prmt(m[6], m[7], 0x40), 0x5410));
+    if (tie == 0.f) {  // true ties, above: an odd code down to the even one
+#pragma unroll 1
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t wi = i < 2 ? v.x : i < 4 ? v.y : i < 6 ? v.z : v.w;
+        const float x = __uint_as_float(i & 1 ? wi & 0xFFFF0000u : wi << 16);
+        const float k = __fadd_rd(x * inv, 12582912.f);
+        const uint32_t odd = fmaf(-((k - 12582912.f) + 0.5f), s, x) == 0.f ? 1u << (8 * (i & 3)) : 0u;
+        if (i < 4)
+          r.x &= ~odd;
+        else
+          r.y &= ~odd;
+      }
+    }
   } else {
     // The conversion rounds t; where t a little smaller and a little larger
     // (2^-22 relative, more than its error) give the same code, x / s does too.
     // Else, pair by pair, the codes around t by its upper bits (below 2^-6,
     // where codes are 2^-9 apart: of t + 2^-6, whose spacing is theirs), up by
-    // one above the middle.
+    // one above the middle, or on it from an odd code.
     const float lo = inv * (1.f - 0x1p-22f), hi = inv * (1.f + 0x1p-22f);
     uint32_t c[4], d[4];
-    float tie = 1.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float x0 = __uint_as_float(w[i] << 16), x1 = __uint_as_float(w[i] & 0xFFFF0000u);
@@ -123,25 +108,13 @@ __device__ __forceinline__ uint2 q8_pack8(const uint4& v, float s, float inv) {
         const uint32_t y = __float_as_uint(u + o);
         const float h = __uint_as_float((y & 0xFFF00000u) | 0x80000u) - o;
         const float e = fmaf(-h, s, fabsf(x));
-        code |= (((y >> 20) - (sub ? 968u : 960u) + 1u + (uint32_t)(__float_as_int(e) >> 31)) |
-                 (__float_as_uint(x) >> 24 & 0x80u))
-                << (8 * k);
-        tie = fminf(tie, fabsf(e));
+        const uint32_t low = (y >> 20) - (sub ? 968u : 960u);
+        const bool up = e > 0.f || (e == 0.f && (low & 1u) != 0);
+        code |= ((low + (up ? 1u : 0u)) | (__float_as_uint(x) >> 24 & 0x80u)) << (8 * k);
       }
       const uint32_t sel = i & 1 ? 0x5410u : 0x3254u;
       uint32_t& half = i < 2 ? r.x : r.y;
       half = prmt(half, code, sel);
-    }
-    rare = tie == 0.f;
-  }
-  if (rare) {  // a true tie: to even
-#pragma unroll 1
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t wi = i < 2 ? v.x : i < 4 ? v.y : i < 6 ? v.z : v.w;
-      const float x = __uint_as_float(i & 1 ? wi & 0xFFFF0000u : wi << 16);
-      const uint32_t b = q8_exact<TYPE>(x, s, x * inv);
-      uint32_t& dst = i < 4 ? r.x : r.y;
-      dst = (dst & ~(255u << (8 * (i & 3)))) | b << (8 * (i & 3));
     }
   }
   return r;
