@@ -78,7 +78,8 @@ __global__ void __launch_bounds__(NT < 128 ? 128 : NT, NT == 512 ? 2 : NT == 256
     }
     uint8_t* dst = (is_v ? a.v_ctx : a.k_ctx) + ((long long)(b * a.Hkv + g) * a.L_cap + p0) * a.dh;
     float* sp = (is_v ? a.v_scale : a.k_scale) + (long long)(b * a.Hkv + g) * a.n_blocks + blk;
-    float s = q8_scale<TYPE>(mx), s_old = s;
+    const float s_own = q8_scale<TYPE>(mx);
+    float s = s_own, s_old = s;
     if (n_old > 0) s_old = *sp;
     // every thread has read the scale before it is written, and `red` before the
     // next group
@@ -100,14 +101,24 @@ __global__ void __launch_bounds__(NT < 128 ? 128 : NT, NT == 512 ? 2 : NT == 256
         reinterpret_cast<uint32_t*>(dst)[i] = r;
       }
     }
-    const float inv = 1.f / s;
-    const bool ok = s == s;
+    const float own = s == s_own ? q8_own_factor<TYPE>(mx, s) : 0.f;
+    if (own != 0.f) {
 #pragma unroll
-    for (int k = 0; k < kVec; ++k) {
-      const int row = row0 + k * step;
-      if (row >= n_old && row < n_end)
-        *reinterpret_cast<uint2*>(dst + (k * NT + tid) * 8) =
-            ok ? q8_pack8<TYPE>(x[k], s, inv) : make_uint2(0, 0);
+      for (int k = 0; k < kVec; ++k) {
+        const int row = row0 + k * step;
+        if (row >= n_old && row < n_end)
+          *reinterpret_cast<uint2*>(dst + (k * NT + tid) * 8) = q8_pack8_own<TYPE>(x[k], own);
+      }
+    } else {
+      const float inv = 1.f / s;
+      const bool ok = s == s;
+#pragma unroll
+      for (int k = 0; k < kVec; ++k) {
+        const int row = row0 + k * step;
+        if (row >= n_old && row < n_end)
+          *reinterpret_cast<uint2*>(dst + (k * NT + tid) * 8) =
+              ok ? q8_pack8<TYPE>(x[k], s, inv) : make_uint2(0, 0);
+      }
     }
     if (tid == 0) *sp = s;
   }
@@ -158,14 +169,20 @@ __device__ __forceinline__ void quant_row(const uint4* __restrict__ src, int K,
 #pragma unroll
   for (int w = 0; w < kQuantThreads / 32; ++w) mx = max(mx, red[w]);
   const float s = q8_scale<TT_Q8_INT8>(mx), inv = 1.f / s;
+  const float own = q8_own_factor<TT_Q8_INT8>(mx, s);
   const bool ok = s == s;
+  auto codes = [&](const uint4& x) {
+    return own != 0.f ? q8_pack8_own<TT_Q8_INT8>(x, own)
+           : ok       ? q8_pack8<TT_Q8_INT8>(x, s, inv)
+                      : make_uint2(0, 0);
+  };
 #pragma unroll
   for (int k = 0; k < kQuantVec; ++k) {
     const int i = k * kQuantThreads + threadIdx.x;
-    if (i < nv) dst[i] = ok ? q8_pack8<TT_Q8_INT8>(v[k], s, inv) : make_uint2(0, 0);
+    if (i < nv) dst[i] = codes(v[k]);
   }
   for (int i = kQuantVec * kQuantThreads + threadIdx.x; i < nv; i += kQuantThreads)
-    dst[i] = ok ? q8_pack8<TT_Q8_INT8>(src[i], s, inv) : make_uint2(0, 0);
+    dst[i] = codes(src[i]);
   if (threadIdx.x == 0) *scale = s;
 }
 

@@ -120,6 +120,45 @@ __device__ __forceinline__ uint2 q8_pack8(const uint4& v, float s, float inv) {
   return r;
 }
 
+// The scale of a group is nearly always that of its own largest magnitude A.  Then
+// x / s = q / (1 + e) with q = x qmax / A and |e| < 2^-23, e the rounding of s
+// alone, and a q that is no middle of two codes is further than 2^-17 from any:
+// q and a middle h are ratios of integers below 2^16 (x and A have 8 bits, qmax 7,
+// h at most 8), so they differ by at least 2^-16 of h.  Every quotient near a
+// middle therefore lies on the same side of it, above for e < 0 and below for e >
+// 0, and x * (1 / s) moved by 2^-22 to that side (more than its three roundings)
+// rounds to the same code.  Returns that factor, or 0 where the group needs
+// q8_pack8: e = 0 (true ties) or the scale is the floor.
+template <int TYPE>
+__device__ __forceinline__ float q8_own_factor(uint32_t amax, float s) {
+  constexpr float kMax = TYPE == TT_Q8_INT8 ? 127.f : 448.f;
+  const float e = fmaf(s, kMax, -bf16_value((uint16_t)amax));
+  const float f = (1.f / s) * (e > 0.f ? 1.f - 0x1p-22f : 1.f + 0x1p-22f);
+  return e == 0.f || !(s > kScaleFloor) ? 0.f : f;
+}
+// Eight values to codes with that factor.
+template <int TYPE>
+__device__ __forceinline__ uint2 q8_pack8_own(const uint4& v, float f) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t m[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float x0 = __uint_as_float(w[i] << 16), x1 = __uint_as_float(w[i] & 0xFFFF0000u);
+    if constexpr (TYPE == TT_Q8_INT8) {
+      // (the low byte of 1.5 * 2^23 + n is n's)
+      m[2 * i] = __float_as_uint(fmaf(x0, f, 12582912.f));
+      m[2 * i + 1] = __float_as_uint(fmaf(x1, f, 12582912.f));
+    } else {
+      m[i] = cvt_e4m3x2(x0 * f, x1 * f);
+    }
+  }
+  if constexpr (TYPE == TT_Q8_INT8)
+    return make_uint2(prmt(prmt(m[0], m[1], 0x40), prmt(m[2], m[3], 0x40), 0x5410),
+                      prmt(prmt(m[4], m[5], 0x40), prmt(m[6], m[7], 0x40), 0x5410));
+  else
+    return make_uint2(prmt(m[0], m[1], 0x5410), prmt(m[2], m[3], 0x5410));
+}
+
 // Largest magnitude of eight bf16 values, merged into two running 16-bit
 // maxima (packed).
 __device__ __forceinline__ uint32_t absmax8(uint32_t m, const uint4& v) {

@@ -96,14 +96,18 @@ def test_scales_grow_block_by_block(kind):
     c.check()
 
 
+# (127 and multiples of 7: the scales of int8 and e4m3 that are exact, so that
+# middles are met)
+@pytest.mark.parametrize("amaxes", [(1.0, 1.9921875, 3.0, 2.0 ** -40 * 1.3125),
+                                    (1.984375, 1.75, 2.0 ** 20 * 2.625, 2.0 ** -30 * 1.984375)])
 @pytest.mark.parametrize("kind", ["int8", "e4m3"])
-def test_every_quotient_rounds_exactly(kind):
+def test_every_quotient_rounds_exactly(kind, amaxes):
     """Values that lie at, next to and between the middles of two codes: bf16
     neighbours of (c + 1/2) s for every code, and the half of the largest."""
     rng = np.random.default_rng(7)
     block, dh = 128, 128
     x = np.empty((4, 4, block, dh))
-    for i, amax in enumerate((1.0, 1.9921875, 3.0, 2.0 ** -40 * 1.3125)):
+    for i, amax in enumerate(amaxes):
         amax = H.bf16(np.array([amax]))[0][0]
         s = float(Q.scale_of(amax, kind)[()])
         v = np.unique(np.abs(Q.values(np.arange(-127, 128).astype(np.int8), kind) if kind == "int8"

@@ -88,3 +88,28 @@ def test_linear_is_the_product_of_dequantised_factors():
     want = (codes * s[:, None].astype(np.float64)) @ (w * ws[:, None].astype(np.float64)).T
     np.testing.assert_allclose(Q.linear(x, w, ws), want, rtol=1e-12)
     assert np.abs(codes * s[:, None].astype(np.float64) - x).max() <= s.max() * 0.5001
+
+
+@pytest.mark.parametrize("kind,qmax", [("int8", 127), ("e4m3", 448)])
+def test_one_factor_rounds_a_group(kind, qmax):
+    """A group under the scale s of its own largest value A: x times 1 / s moved by
+    2^-22 against the sign of s - A / qmax rounds to the exact code, for every
+    pair of significands, unless s is exact."""
+    f32, exact = np.float32, 0
+    x_all = (np.arange(128, 256)[:, None] / 128.0 * np.exp2(np.arange(-20.0, 1.0))).ravel()
+    for m in range(128, 256):
+        A = m / 128.0
+        s = Q.scale_of(A, kind)[()]
+        e = np.float64(s) * qmax - A
+        if e == 0:
+            exact += 1
+            continue
+        f = f32(f32(1) / s * f32(1 - np.copysign(2.0 ** -22, e)))
+        x = x_all[x_all <= A].astype(f32)
+        want = Q.values(Q.encode(x, s, kind), kind)
+        if kind == "int8":                 # one rounding, of x * f + 1.5 * 2^23
+            got = np.rint(x.astype(np.float64) * np.float64(f))
+        else:                              # x * f to fp32, that to a code
+            got = Q.values(Q.encode(x * f, f32(1), kind), kind)
+        np.testing.assert_array_equal(got, want)
+    assert exact in ((1, 2, 3) if kind == "int8" else range(1, 20))
