@@ -149,8 +149,8 @@ LinearWs carve_linear(int rows, int K, void* ws) {
 // 128 columns are no more than the SMs, each tile goes to a cluster of `splits`
 // CTAs that share its K: of the shapes that fit, the one whose CTAs read the
 // fewest bytes, an exchange of partial sums counted as 200 KB (about 1 us).
-// 128 x 4608, K = 4096: 72 tiles of 64 in pairs 11.5 us, 144 of 32 alone 12.6,
-// 36 of 128 in fours 16.8 (clusters of four leave SMs of a GPC over, so not
+// 128 x 4608, K = 4096: 72 tiles of 64 in pairs 10.4 us, 144 of 32 alone 12.0,
+// 36 of 128 in fours 16.0 (clusters of four leave SMs of a GPC over, so not
 // all 36 run at once: more than two CTAs only within 7/8 of the SMs).
 // splits = 0: more tiles than SMs; 256-wide tiles, one CTA each in turn, which
 // read A less often.
@@ -178,9 +178,9 @@ I8Shape i8_shape(int rows, int N, int K) {
 }
 
 // The persistent linear update: pairs of CTAs on 256-row tiles where there is more
-// than one 128-row tile, also where the last pair has one (K = 4096; 2048 x 4608:
-// 36.5 us against 44.5 for CTAs on their own; 200 x 40000: 47 against 58; 300 x
-// 40000: 66 against 69).  The vocabulary step, whose row count only the GPU knows,
+// than one 128-row tile (K = 4096; 2048 x 4608: 34.2 us against 37.5 for CTAs on
+// their own; 1024 x 6400: 32 against 39; 200 x 40000: 48 against 52), also where
+// the last pair has one (300 x 40000: 63 against 67; 384 x 20000: 41 against 39).  The vocabulary step, whose row count only the GPU knows,
 // keeps CTAs on their own: pairs gain 3 % at 1024 rows of 1024 and lose 20 % when
 // 100 of them are masked.
 bool i8_pair(int rows) { return rows > kI8BM; }

@@ -1,10 +1,10 @@
 // Writers of 8-bit data: rows joining an 8-bit context cache, and rows
 // quantised one by one for the integer products.  Both read each bf16 value
 // once (a group stays in registers between its maximum and its rounding): 2
-// bytes in and 1 byte out per value, all that HBM has to carry.  The append's
-// exact rounding costs more instructions than that time holds: 16 prompts of up
-// to 8192 tokens, 2 KV heads of dh 128, take 56 us as e4m3, 2.7 TB/s; 16 rows onto
-// each of 64 sequences 6.3 us, most of it the two launches.
+// bytes in and 1 byte out per value, all that HBM has to carry.  16 prompts of up to
+// 8192 tokens, 2 KV heads of dh 128, blocks of 64, take 36 us as e4m3 (4.1 TB/s),
+// a third of it instructions that the loads do not hide; 16 rows onto each of 64
+// sequences 6.3 us, most of it the two launches.
 #include <algorithm>
 
 #include "tt_q8.h"
@@ -17,8 +17,7 @@ namespace {
 // A thread holds kVec vectors of 8 values of one cache block, so a block of
 // block * dh values takes 32 (16 x 64) to 512 (128 x 128) threads.  A CTA has at
 // least 128 threads, several blocks side by side where they are small.  (With
-// 8 vectors: 58 us against 56 for 16 prompts of up to 8192 tokens, the longer
-// code costing more than the shorter prologue saves.)
+// 8 vectors: 40 us against 36 for 16 prompts of up to 8192 tokens; with 2: 60.)
 constexpr int kVec = 4;
 
 // How many rows sequence b gets, or -1 when its lengths are out of range.

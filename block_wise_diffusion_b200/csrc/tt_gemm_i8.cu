@@ -19,7 +19,7 @@
 //
 // What bounds them: few rows, the weights' bytes from HBM (77 masked rows, V =
 // 131072, H = 4096: 92 us with quantisation and commit, 5.8 TB/s; 128 x 4608, K =
-// 4096, is too short for that: 11.5 us, 3 of them the rows' quantisation); many
+// 4096, is too short for that: 10.4 us, 2 of them the rows' quantisation); many
 // rows, the tensor cores at the clock that the power limit leaves (1024 rows of the
 // same vocabulary step: 380 us, 2.9 PFLOP/s of integer products).
 //
