@@ -29,8 +29,10 @@
 // passes, 13,000 cycles when nothing hides them) then runs under the softmax of
 // the tiles before (48 sequences of up to 32768 keys: 219 us; as first tile 239).
 // What bounds it: a tile of both chains is 2,050 cycles of tensor work and as many
-// of exponentials, which the conversion, the maxima and the waits between them
-// stretch to 3,500.  4 sequences of 65536 int8 keys, S = 16, 2 KV heads of 16
+// of exponentials, but the hand-overs between the roles (S twice per tile through
+// one buffer, P to its product, the codes' reload and conversion) are loops of about
+// 3,200 cycles each: without exponentials, conversion and all but one MMA of eight,
+// the time falls by a quarter only.  4 sequences of 65536 int8 keys, S = 16, 2 KV heads of 16
 // queries and dh 128, with the merge: 78 us, 880 TFLOP/s and 1.7 TB/s of cache.
 // Few tiles per CTA pay the start instead: 8 x 4096 keys, 32 us.
 // Roles (16 warps; registers are moved to the softmax by setmaxnreg):
@@ -305,9 +307,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
       if (first < sb) {
         // The warp's 32 query rows, each by a power of two in fp16 range: a row
         // to DH / 8 lanes, so that loads are whole lines (a row to a thread
-        // took 8,000 cycles, these 2,000), eight in flight: all sixteen of dh 128
-        // at once unroll to more instructions than they save (+7 % on long caches).  The previous
-        // segment's last S of this chain has been waited for below.
+        // took 8,000 cycles), eight in flight: all sixteen of dh 128 at once
+        // unroll to more instructions than they save (+7 % on long caches).  The
+        // previous segment's last S of this chain has been waited for below.
         float c_row = 0.f;
         {
           constexpr int LPR = DH / 8, RPL = 32 / LPR;  // lanes per row, rows per load
