@@ -86,13 +86,19 @@ __device__ __forceinline__ void stage_scales(float* cs, const float* b_scale, in
 }
 
 // One row's 32 columns (or `lim` of them): integer sums r to bf16, times the
-// row's scale rs and the columns' cs.  vec: 32- or 16-byte stores where every
-// row is that aligned (2, 1), 0: single values.
+// row's scale rs and the columns' cs; dst: the row's first of them.  vec: 32- or
+// 16-byte stores where every row is that aligned (2, 1).  Other N (0): through the
+// warp's own `stage`, so that a store is a run of one or two rows (2048 x 4607, K =
+// 4096: 45 us; single values, a lane to a row, took 121).  All lanes take part, row0
+// is the first lane's row.
+constexpr int kStageWords = 32 * 17;  // a row to 17 words: no bank conflicts
 __device__ __forceinline__ int store_width(const uint16_t* C, int N) {
   return (N & 15) == 0 && (reinterpret_cast<uintptr_t>(C) & 31) == 0 ? 2 : (N & 7) == 0 ? 1 : 0;
 }
 __device__ __forceinline__ void store_row32(const uint32_t (&r)[32], float rs, const float* cs,
-                                            uint16_t* dst, int lim, bool valid, int vec) {
+                                            uint16_t* dst, int lim, int row0, int M, int N, int vec,
+                                            uint32_t* stage) {
+  const int lane = threadIdx.x & 31;
   uint32_t w[16];
 #pragma unroll
   for (int j = 0; j < 32; j += 4) {
@@ -100,7 +106,26 @@ __device__ __forceinline__ void store_row32(const uint32_t (&r)[32], float rs, c
     w[j / 2] = pack_bf16x2((float)(int)r[j] * (rs * c.x), (float)(int)r[j + 1] * (rs * c.y));
     w[j / 2 + 1] = pack_bf16x2((float)(int)r[j + 2] * (rs * c.z), (float)(int)r[j + 3] * (rs * c.w));
   }
-  if (!valid) return;
+  if (vec == 0) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) stage[lane * 17 + j] = w[j];
+    __syncwarp();
+    uint16_t* d0 = dst - (ptrdiff_t)lane * N;  // row0's
+    const int rows = min(32, M - row0);
+    if ((N & 1) == 0) {
+      for (int i = lane >> 4; i < rows; i += 2)
+        if (2 * (lane & 15) < lim)
+          *reinterpret_cast<uint32_t*>(d0 + (ptrdiff_t)i * N + 2 * (lane & 15)) =
+              stage[i * 17 + (lane & 15)];
+    } else {
+      for (int i = 0; i < rows; ++i)
+        if (lane < lim)
+          d0[(ptrdiff_t)i * N + lane] = (uint16_t)(stage[i * 17 + (lane >> 1)] >> ((lane & 1) * 16));
+    }
+    __syncwarp();
+    return;
+  }
+  if (row0 + lane >= M) return;
   if (vec == 2) {
 #pragma unroll
     for (int v = 0; v < 2; ++v)
@@ -109,16 +134,12 @@ __device__ __forceinline__ void store_row32(const uint32_t (&r)[32], float rs, c
                      "r"(w[8 * v]), "r"(w[8 * v + 1]), "r"(w[8 * v + 2]), "r"(w[8 * v + 3]),
                      "r"(w[8 * v + 4]), "r"(w[8 * v + 5]), "r"(w[8 * v + 6]), "r"(w[8 * v + 7])
                      : "memory");
-  } else if (vec == 1) {
+  } else {
 #pragma unroll
     for (int v = 0; v < 4; ++v)
       if (v * 8 < lim)
         reinterpret_cast<uint4*>(dst)[v] =
             make_uint4(w[4 * v], w[4 * v + 1], w[4 * v + 2], w[4 * v + 3]);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 32; ++j)
-      if (j < lim) dst[j] = (uint16_t)(w[j >> 1] >> ((j & 1) * 16));
   }
 }
 
@@ -127,7 +148,7 @@ __device__ __forceinline__ void store_row32(const uint32_t (&r)[32], float rs, c
 template <int EPI>
 __device__ __forceinline__ void drain_tile(const GemmI8Args& a, uint32_t tbase, int row, int M,
                                            float rs, const float* cs, int n, int num_n, int col0,
-                                           int ncols) {
+                                           int ncols, uint32_t* stage) {
   const int nchunks = (ncols + 31) >> 5;
   if constexpr (EPI == 0) {
     // Per row: the maximum of sum * column scale, the sum of exponentials
@@ -180,7 +201,8 @@ __device__ __forceinline__ void drain_tile(const GemmI8Args& a, uint32_t tbase, 
       uint32_t r[32];
       tmem_ld32(tbase + ch * 32, r);
       tmem_wait_ld();
-      store_row32(r, rs, cs + ch * 32, dst + ch * 32, ncols - ch * 32, row < M, vec);
+      store_row32(r, rs, cs + ch * 32, dst + ch * 32, ncols - ch * 32, row - (threadIdx.x & 31), M,
+                  a.N, vec, stage);
     }
   }
 }
@@ -335,7 +357,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       if (!mbar_wait(&accf[acc], acc_phase, a.err, abort_flag, WHERE_GEMM_EPI)) break;
       tc_fence_after();
       const uint32_t tbase = tmem + acc * BN + ((uint32_t)(q * 32) << 16);
-      drain_tile<EPI>(a, tbase, row, M, rs, cs, n, num_n, col0, ncols);
+      drain_tile<EPI>(a, tbase, row, M, rs, cs, n, num_n, col0, ncols,
+                      reinterpret_cast<uint32_t*>(scales + 4 * BN) + q * kStageWords);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&acce[acc]);
@@ -558,7 +581,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       if (!mbar_wait(&accf[acc], acc_phase, a.err, abort_flag, WHERE_GEMM_EPI)) break;
       tc_fence_after();
       drain_tile<1>(a, tmem + acc * BN + ((uint32_t)(q * 32) << 16), row, M, rs, cs, n, num_n, col0,
-                      ncols);
+                      ncols,
+                    reinterpret_cast<uint32_t*>(scales + 4 * BN) + q * kStageWords);
       tc_fence_before();
       __syncwarp();
       if (lane == 0)
@@ -774,7 +798,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             r[4 * v + 3] += x.w;
           }
       }
-      store_row32(r, rs, cs + c0, a.C + (size_t)row * a.N + col, lim, row < a.M_alloc, vec);
+      // (the ring is free by now)
+      store_row32(r, rs, cs + c0, a.C + (size_t)row * a.N + col, lim, row - lane, a.M_alloc, a.N, vec,
+                  reinterpret_cast<uint32_t*>(sA) + q * kStageWords);
     }
   }
   tc_fence_before();
@@ -788,7 +814,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 template <int EPI, int BN, int STAGES>
 cudaError_t launch_gemm_i8(const CUtensorMap& tmA, const CUtensorMap& tmB, const GemmI8Args& a,
                            int grid, cudaStream_t st) {
-  constexpr size_t smem = (size_t)STAGES * (kI8BM + BN) * kI8BK + 1024 + 256 + 4 * BN * 4;
+  constexpr size_t smem = (size_t)STAGES * (kI8BM + BN) * kI8BK + 1024 + 256 + 4 * BN * 4 +
+                          (EPI == 1 ? 4 * kStageWords * 4 : 0);
   static_assert(smem <= 232448, "shared memory per CTA");
   static_assert(2 * BN <= 512, "two accumulators must fit TMEM");
   const cudaError_t e = allow_smem<gemm_i8_kernel<EPI, BN, STAGES>>(smem);
@@ -823,7 +850,8 @@ static cudaError_t launch_cluster(Kern kern, int grid, int cluster, size_t smem,
 template <int BN, int STAGES>
 static cudaError_t launch_gemm_i8_pair(const CUtensorMap& tmA, const CUtensorMap& tmB,
                                        const GemmI8Args& a, int pairs, cudaStream_t st) {
-  constexpr size_t smem = (size_t)STAGES * (kI8BM + BN / 2) * kI8BK + 1024 + 256 + 4 * BN * 4;
+  constexpr size_t smem = (size_t)STAGES * (kI8BM + BN / 2) * kI8BK + 1024 + 256 + 4 * BN * 4 +
+                          4 * kStageWords * 4;
   static_assert(smem <= 232448, "shared memory per CTA");
   static_assert(2 * BN <= 512, "two accumulators must fit TMEM");
   const cudaError_t e = allow_smem<gemm_i8_pair_kernel<BN, STAGES>>(smem);

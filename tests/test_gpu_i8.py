@@ -58,7 +58,7 @@ def linear(rows, N, K, seed, extreme=False):
     (300, 1000, 2000), (5, 4608, 4096), (1, 9000, 4096), (64, 513, 8192), (2000, 72, 320), (3, 24, 131072),
     (257, 1024, 144), (128, 128, 16384),
     (300, 13001, 144), (257, 26000, 2064), (2100, 2600, 256), (1025, 6400, 128),
-    (40000, 24, 64), (20000, 1, 16)])
+    (40000, 24, 64), (20000, 1, 16), (5, 20001, 64), (130, 20002, 48), (65, 65, 1040)])
 def test_linear_matches_oracle(rows, N, K):
     linear(rows, N, K, rows + N + K)
 
@@ -83,7 +83,7 @@ def test_linear_zero_and_non_finite_rows():
 def test_linear_writes_only_its_output():
     from tests.test_gpu_guards import Guarded, _check
     rng = np.random.default_rng(1)
-    for rows, N, K in ((17, 389, 112), (128, 520, 512), (40, 24, 4096)):
+    for rows, N, K in ((17, 389, 112), (128, 520, 512), (40, 24, 4096), (300, 13001, 64), (5, 20002, 64)):
         ins = dict(x=Guarded((rows, K), torch.bfloat16, H.up_bf16(H.bf16(rng.standard_normal((rows, K)))[1])),
                    w=Guarded((N, K), torch.int8, H.up(rng.integers(-127, 128, (N, K)).astype(np.int8))),
                    s=Guarded((N,), torch.float32, H.up(rng.random(N).astype(np.float32))))
