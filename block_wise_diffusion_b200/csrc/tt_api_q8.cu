@@ -84,7 +84,7 @@ struct Carver {
 struct AttnQ8Ws {
   int* ctrl;
   int2* unit_span;
-  float *part_o, *part_ml;
+  float *part_o, *part_lse;
   size_t total;
 };
 AttnQ8Ws carve_attn(const tt_dims& d, const AttnShape& g, void* ws) {
@@ -95,7 +95,7 @@ AttnQ8Ws carve_attn(const tt_dims& d, const AttnShape& g, void* ws) {
   w.ctrl = c.take<int>(kCtrlBytes);
   w.unit_span = c.take<int2>((size_t)g.units * sizeof(int2));
   w.part_o = c.take<float>(slots * rows * d.dh * sizeof(float));
-  w.part_ml = c.take<float>(slots * rows * 2 * sizeof(float));
+  w.part_lse = c.take<float>(slots * rows * sizeof(float));
   w.total = c.total();
   return w;
 }
@@ -276,7 +276,7 @@ tt_status tt_block_denoise_attn_q8(const tt_dims* d, const tt_q8* f, const tt_bf
   a.n_ctas = g.n_ctas;
   a.unit_span = w.unit_span;
   a.part_o = w.part_o;
-  a.part_ml = w.part_ml;
+  a.part_lse = w.part_lse;
   a.err = w.ctrl;
   if (d->S * g.G <= kRowsMax) {
     Q8_LAUNCH(TT_K_ATTN_Q8, st, launch_attn_q8_rows(a, f->type, st));

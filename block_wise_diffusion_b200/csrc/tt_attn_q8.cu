@@ -68,7 +68,7 @@ __host__ __device__ constexpr Smem smem_layout(int dh) {
   s.raw = s.v + kSlots * nsub * kSub;    // codes of one K and one V tile
   s.scales = s.raw + 2 * kAttnBN * dh;  // [slot][key scale, log2 w, 1 / w][8 groups]
   s.bars = (s.scales + kSlots * 24 * 4 + 63) / 64 * 64;
-  s.total = s.bars + 256;
+  s.total = s.bars + 320;
   return s;
 }
 
@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
     if (walk.off > 0) {  // an empty range inside a unit: an empty record
       const size_t slot = (size_t)walk.b * U + walk.k + blockIdx.x;
       for (int i = threadIdx.x; i < 256; i += kThreads)
-        reinterpret_cast<float2*>(a.part_ml)[slot * 256 + i] = make_float2(-INFINITY, 0.f);
+        a.part_lse[slot * 256 + i] = -INFINITY;
     }
     return;
   }
@@ -227,7 +227,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
   uint64_t* sc_full = empty + 2 * kSlots;  // [slot]
   uint64_t* rk_full = sc_full + kSlots;  // [K, V] a tile of codes has landed
   uint64_t* rk_empty = rk_full + 2;      // [K, V] it has been converted
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(rk_empty + 2);
+  uint64_t* own_full = rk_empty + 2;     // [slot] the own keys' and values' exponents
+  int2* own_exp = reinterpret_cast<int2*>(own_full + kSlots);  // [slot]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(own_exp + kSlots);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
   uint32_t* red = tmem_slot + 2;  // [8] converter reduction
 
@@ -250,6 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
         mbar_init(&empty[2 * kv + s], 1);
       }
       mbar_init(&sc_full[s], 8);
+      mbar_init(&own_full[s], 1);
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -403,10 +406,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
           }
           need = mx > m + kRescale;
           if (need) {
-            alpha = ex2(m - mx);
+            const float half = ex2(0.5f * (m - mx));
+            alpha = half * half;
+            l = l * half * half;
             m = mx;
           }
-          l *= alpha;
           exps16(s, kf[0], lw[0], iw[0], c_row, m, l, p0);
           exps16(s + 16, kf[1], lw[1], iw[1], c_row, m, l, p1);
           // P and O are the tensor core's until P . V of the turn before has run
@@ -457,8 +461,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
         tc_fence_after();
       }
       // A unit that this CTA holds alone, in rows of its own, is done; other
-      // segments leave a partial: unnormalised O (tile-major [dh/4][256
-      // rows][4], a warp's store is 512 contiguous bytes) and (m, l).
+      // segments leave a record: their output (tile-major [dh/4][256 rows][4],
+      // a warp's store is 512 contiguous bytes) and log2 of their sum.
       const int r256 = ch * 128 + r;
       const bool ends = sb == 1 + (L + kAttnBN - 1) / kAttnBN;
       const bool whole = !split && sa == 0 && ends;
@@ -484,13 +488,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
 #pragma unroll
             for (int v = 0; v < 8; ++v)
               *reinterpret_cast<float4*>(po + (size_t)(c0 / 4 + v) * 1024) =
-                  make_float4(__uint_as_float(o[4 * v]), __uint_as_float(o[4 * v + 1]),
-                              __uint_as_float(o[4 * v + 2]), __uint_as_float(o[4 * v + 3]));
+                  make_float4(__uint_as_float(o[4 * v]) * inv, __uint_as_float(o[4 * v + 1]) * inv,
+                              __uint_as_float(o[4 * v + 2]) * inv,
+                              __uint_as_float(o[4 * v + 3]) * inv);
           }
         }
       }
-      if (valid && !whole)
-        reinterpret_cast<float2*>(a.part_ml)[slot * 256 + r256] = make_float2(m, l);
+      if (valid && !whole) a.part_lse[slot * 256 + r256] = m + log2f(l);
     }
   } else if (warp < 12) {
     // ---------------------------------------------- codes to fp16 tiles
@@ -531,9 +535,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
         }
       }
     };
-    // The block's own rows [S, Hkv, dh] (bf16) by a power of two in fp16
-    // range; returns its exponent.  Rows past S are zero.
-    auto block_rows = [&](const uint16_t* p, uint32_t dst, int slot_id) -> int {
+    // The block's own keys or values (kv) [S, Hkv, dh] (bf16) by a power of two
+    // in fp16 range; the exponents go to warp 15.  Rows past S are zero.
+    int ek = 0;
+    auto block_rows = [&](const uint16_t* p, uint32_t dst, int kv, int slot) {
       constexpr int NB = kAttnBN * DH / 8 / kConv;
       uint32_t mx = 0;
       const int c0 = tid % (DH / 8), r0 = tid / (DH / 8);
@@ -547,10 +552,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
       }
       mx = __reduce_max_sync(0xffffffffu, max(mx & 0xFFFFu, mx >> 16));
       named_bar_sync(1, kConv);  // the previous use of red is over
-      if (lane == 0) red[(warp - 8) + 4 * slot_id] = mx;
+      if (lane == 0) red[(warp - 8) + 4 * kv] = mx;
       named_bar_sync(1, kConv);
-      const uint32_t* rd = red + 4 * slot_id;
-      const int e = norm_exp(max(max(rd[0], rd[1]), max(rd[2], rd[3])));
+      const uint32_t* rd = red + 4 * kv;
+      const uint32_t top = max(max(rd[0], rd[1]), max(rd[2], rd[3]));
+      const int e = kv ? own_value_exp(top) : norm_exp(top);
+      if (tid == 0 && kv) {
+        own_exp[slot] = make_int2(ek, e);
+        mbar_arrive(&own_full[slot]);
+      }
+      ek = e;
       const float f = pow2i(-e);
 #pragma unroll 4
       for (int i = 0; i < NB; ++i) {
@@ -561,7 +572,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
         sts128(dst + chunk_at(row, c0), bf16x2_to_f16x2(x.x, f), bf16x2_to_f16x2(x.y, f),
                bf16x2_to_f16x2(x.z, f), bf16x2_to_f16x2(x.w, f));
       }
-      return e;
     };
     int kt = 0, used0 = 0, used1 = 0;  // tiles, uses of each slot
     int raw = 0;                       // context tiles so far
@@ -575,7 +585,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
         const uint32_t par = ((uint32_t)(slot ? used1++ : used0++) & 1u) ^ 1u;
         const int nv = tile_keys(tl, L, a.S);
         const bool ctx = is_context(tl, L);
-        int ek = 0;  // exponent of the block's K rows
 #pragma unroll 1
         for (int kv = 0; kv < 2; ++kv) {  // K, then V
           if ((ctx && !mbar_wait_inline(&rk_full[kv], (uint32_t)raw & 1u, a.err, abort_flag,
@@ -587,12 +596,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
           }
           const uint32_t dst = sK + (kv * kSlots + slot) * NSUB * kSub;
           if (!ctx) {
-            const int e = block_rows((kv ? a.v_blk : a.k_blk) +
-                                         ((size_t)ub * a.S * a.Hkv + ug) * DH, dst, kv);
-            // the block's scales; V's slot, once free, frees the scales' too
-            if (kv == 1 && tid < 8)
-              put_scales(scales + slot * 24, tid, pow2i(ek), (float)e, pow2i(-e), &sc_full[slot]);
-            ek = e;
+            block_rows((kv ? a.v_blk : a.k_blk) + ((size_t)ub * a.S * a.Hkv + ug) * DH, dst, kv,
+                       slot);
           } else {
             convert(rK + kv * kAttnBN * DH, dst, nv);
             mbar_arrive(&rk_empty[kv]);
@@ -637,19 +642,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
         }
       }
     } else if (warp == 15) {
-      // ------------------------------------ scales of the context tiles
+      // -------------------------------------------- scales of the tiles
       // Lane g < 8: 16 keys.  A tile's scales go with its V slot: once P . V of
-      // the tile that had the slot before has run, its softmax is done.
-      int kt = 0, used0 = 0, used1 = 0;
+      // the tile that had the slot before has run, its softmax is done.  A value
+      // scale is held at 2^-100 of the segment's largest so far (tt_attn_q8.cuh).
+      int kt = 0, used0 = 0, used1 = 0, own0 = 0, own1 = 0;
       bool ok = true;
       while (ok && walk.next(ub, uk, sa, sb, L)) {
         const size_t pair = (size_t)ub * a.Hkv + uk / a.n_qtiles;
         const float* ksp = a.k_scale + pair * a.n_blocks;
         const float* vsp = a.v_scale + pair * a.n_blocks;
-        float nk = 1.f, nw = 1.f;  // a tile ahead
+        float nk = 1.f, nw = 1.f, top = 0.f;  // a tile ahead
+        bool in = false;
         auto load = [&](int tl) {
           const int pos = tl * kAttnBN + lane * 16;
-          const bool in = lane < 8 && tl < sb && pos < L;
+          in = lane < 8 && tl < sb && pos < L;
           nk = in ? __ldg(ksp + (pos >> a.block_shift)) : 1.f;
           nw = in ? __ldg(vsp + (pos >> a.block_shift)) : 1.f;
         };
@@ -657,11 +664,25 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
         for (int tl = sa; tl < sb; ++tl, ++kt) {
           const int slot = split ? (tl - sa) & 1 : kt & 1;
           const uint32_t par = ((uint32_t)(slot ? used1++ : used0++) & 1u) ^ 1u;
+          float w = in ? nw : 0.f;
+#pragma unroll
+          for (int o = 4; o > 0; o >>= 1) w = fmaxf(w, __shfl_xor_sync(0xffffffffu, w, o));
+          top = fmaxf(top, w);
+          float kf = nk, lw = log2f(value_scale(nw, top)), iw = 1.f / value_scale(nw, top);
+          load(tl + 1);
           ok = mbar_wait_inline(&empty[2 + slot], par, a.err, abort_flag, WHERE_ATTN_PRODUCER);
           if (!ok) break;
-          if (is_context(tl, L) && lane < 8)
-            put_scales(scales + slot * 24, lane, nk, log2f(nw), 1.f / nw, &sc_full[slot]);
-          load(tl + 1);
+          if (!is_context(tl, L)) {
+            ok = mbar_wait_inline(&own_full[slot], (uint32_t)(slot ? own1++ : own0++) & 1u, a.err,
+                                  abort_flag, WHERE_ATTN_PRODUCER);
+            if (!ok) break;
+            const int2 e = own_exp[slot];
+            w = value_scale(pow2i(e.y), top);
+            kf = pow2i(e.x);
+            lw = log2f(w);
+            iw = 1.f / w;
+          }
+          if (lane < 8) put_scales(scales + slot * 24, lane, kf, lw, iw, &sc_full[slot]);
           __syncwarp();
         }
       }
@@ -758,11 +779,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
   }
 }
 
-// The segment partials of a unit that several CTAs hold (two per segment where
-// the chains split the tiles) into the bf16 output.  Block = (unit, 32 query
-// rows, 1 / parts of the columns), lane = row, NG groups of 4 columns to a
-// warp, whose loads are 512 contiguous bytes.  One pass with a running maximum;
-// the loads of KB records are in flight together, for latency is all there is.
+// The records of a unit that several CTAs hold (two per segment where the chains
+// split the tiles) into the bf16 output: sum_c 2^(lse_c) o_c / sum_c 2^(lse_c).
+// Block = (unit, 32 query rows, 1 / parts of the columns), lane = row, NG groups
+// of 4 columns to a warp, whose loads are 512 contiguous bytes.  One pass with a
+// running maximum; the loads of KB records are in flight together, for latency
+// is all there is.
 template <int NG, int KB>
 __global__ void __launch_bounds__(256) attn_q8_merge_kernel(const AttnQ8Args a) {
   griddep_launch();
@@ -777,7 +799,7 @@ __global__ void __launch_bounds__(256) attn_q8_merge_kernel(const AttnQ8Args a) 
   if (rb * 32 - h * 128 >= a.rows_per_half) return;  // no rows in this block
   const int n = (uc.y - uc.x + 1) * per;
   const size_t slot0 = (size_t)u + uc.x;
-  const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + slot0 * 256;
+  const float* lse = a.part_lse + slot0 * 256;
   const float4* po = reinterpret_cast<const float4*>(a.part_o) + slot0 * ngrp * 256;
   // record c: row of the segment's 256 (its chain's 128 where the chains split)
   auto at = [&](int c) { return per == 2 ? (c & 1) * 128 + r : row; };
@@ -789,23 +811,23 @@ __global__ void __launch_bounds__(256) attn_q8_merge_kernel(const AttnQ8Args a) 
   for (int g = 0; g < NG; ++g) acc[g] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
   for (int c0 = 0; c0 < n; c0 += KB) {
-    float2 x[KB];
+    float x[KB];
     float4 o[KB][NG];
 #pragma unroll
     for (int k = 0; k < KB; ++k) {
       const int c = min(c0 + k, n - 1);
-      x[k] = __ldg(ml + rec(c) * 256 + at(c));
+      x[k] = __ldg(lse + rec(c) * 256 + at(c));
 #pragma unroll
       for (int g = 0; g < NG; ++g) o[k][g] = __ldcg(po + (rec(c) * ngrp + g0 + g) * 256 + at(c));
     }
 #pragma unroll
     for (int k = 0; k < KB; ++k) {
       // past the last record, or one without keys (its output was never written)
-      if (c0 + k >= n || x[k].y == 0.f) continue;
-      const float mn = x[k].x > mx ? x[k].x : mx;
-      const float f0 = ex2(mx - mn), f1 = ex2(x[k].x - mn);
+      if (c0 + k >= n || x[k] == -INFINITY) continue;
+      const float mn = x[k] > mx ? x[k] : mx;
+      const float f0 = ex2(mx - mn), f1 = ex2(x[k] - mn);
       mx = mn;
-      den = fmaf(den, f0, x[k].y * f1);
+      den = fmaf(den, f0, f1);
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
         acc[g].x = fmaf(acc[g].x, f0, o[k][g].x * f1);

@@ -130,6 +130,27 @@ __device__ __forceinline__ int norm_exp(uint32_t amax) {
   const int e = (int)(amax >> 7);
   return e == 0 || e == 255 ? 0 : min(max(e - 127 - 14, -126), 126);
 }
+
+// Ranges.  With m the running maximum of s_j + log2 w_j, a key's part of the row
+// sum is 2^(s_j - m) = p_j / w_j.  Three things keep it what it is:
+//  - w >= 2^-100 (the cache's scales are at least 2^-60, the own values' exponent
+//    is held there: values below 2^-114 lose bits, below 2^-125 they are 0), so that
+//    the sum stays below 2^127;
+//  - p_j is 0 below 2^-126, where p_j / w_j may still count, so w is also held at
+//    2^-100 of the largest so far: m <= max s + max log2 w leaves every key of weight
+//    2^-26 and more a p that is a number, and what is held moves a value by
+//    2^-85 of the largest at most;
+//  - a new maximum can move the sum by 2^-220, which is no number either: by its
+//    square root, twice.
+// A record is a segment's own normalised output with log2 of its sum, m + log2 l,
+// in which w no longer occurs.
+constexpr int kOwnLow = -100;
+__device__ __forceinline__ int own_value_exp(uint32_t amax) { return max(norm_exp(amax), kOwnLow); }
+// (NaN stays NaN)
+__device__ __forceinline__ float value_scale(float w, float top) {
+  const float low = top * 0x1p-100f;
+  return w < low ? low : w;
+}
 // Two running maxima (packed) of bf16 magnitudes.
 __device__ __forceinline__ uint32_t absmax_bf16x8(uint32_t m, const uint4& v) {
   m = __vmaxu2(m, v.x & 0x7FFF7FFFu);

@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_rows_kernel(const AttnQ8A
   griddep_wait();
   extern __shared__ __align__(16) float sm_o[];  // [warp][16][DH + 4]
   __shared__ PlanSmem plan;
-  __shared__ float sm_m[kWarps][16], sm_l[kWarps][16];
+  __shared__ float sm_lse[kWarps][16], sm_inv[kWarps][16];
   constexpr int KW = DH / 16;  // words of a key per lane (K side), steps of Q K^T
   constexpr int VW = DH / 32;  // words of a key per lane (V side)
   constexpr int NT = DH / 8;   // column tiles of O
@@ -79,8 +79,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_rows_kernel(const AttnQ8A
   if (walk.left == 0) {
     if (walk.off > 0) {  // an empty range inside a unit: an empty record
       const size_t slot = (size_t)walk.b * a.Hkv + walk.k + blockIdx.x;
-      if (threadIdx.x < 16)
-        reinterpret_cast<float2*>(a.part_ml)[slot * 16 + threadIdx.x] = make_float2(-INFINITY, 0.f);
+      if (threadIdx.x < 16) a.part_lse[slot * 16 + threadIdx.x] = -INFINITY;
     }
     return;
   }
@@ -92,7 +91,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_rows_kernel(const AttnQ8A
     float o[NT][4];
 #pragma unroll
     for (int j = 0; j < NT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, w_top = 0.f;
 
     // Softmax of NTILE 8-key tiles of scores (16 keys share a scale) and its
     // product with V: `vfrag(t16, j, b0, b1)` gives the operands of keys
@@ -124,14 +123,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_rows_kernel(const AttnQ8A
         mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
         alpha[h] = 1.f;
         if (mx[h] > m[h] + kRescale) {
-          alpha[h] = ex2(m[h] - mx[h]);
+          const float half = ex2(0.5f * (m[h] - mx[h]));
+          alpha[h] = half * half;
+          l[h] = l[h] * half * half;
           m[h] = mx[h];
           need = true;
         }
       }
       if (__any_sync(0xffffffffu, need)) {
-        l[0] *= alpha[0];
-        l[1] *= alpha[1];
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
           o[j][0] *= alpha[0];
@@ -263,8 +262,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_rows_kernel(const AttnQ8A
         }
       }
       const int ek = norm_exp(__reduce_max_sync(0xffffffffu, max(mk & 0xFFFFu, mk >> 16)));
-      const int ev = norm_exp(__reduce_max_sync(0xffffffffu, max(mv & 0xFFFFu, mv >> 16)));
+      const int ev = own_value_exp(__reduce_max_sync(0xffffffffu, max(mv & 0xFFFFu, mv >> 16)));
       const float fk = pow2i(-ek), fv = pow2i(-ev);
+      w_top = pow2i(ev);
       float s[2][4];
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
@@ -293,9 +293,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_rows_kernel(const AttnQ8A
       float sk[NG], lw[NG], iw[NG];
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
+        w_top = fmaxf(w_top, nvs[g]);  // (1 past the end: harmless)
+        const float w = value_scale(nvs[g], w_top);
         sk[g] = nks[g];
-        lw[g] = log2f(nvs[g]);
-        iw[g] = 1.f / nvs[g];
+        lw[g] = log2f(w);
+        iw[g] = 1.f / w;
       }
       float s[2 * NG][4];
 #pragma unroll
@@ -340,8 +342,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_rows_kernel(const AttnQ8A
       l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
       l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
       if (c4 == 0) {
-        sm_m[warp][n8 + 8 * h] = m[h];
-        sm_l[warp][n8 + 8 * h] = l[h];
+        sm_lse[warp][n8 + 8 * h] = m[h] + log2f(l[h]);  // -inf without keys
+        sm_inv[warp][n8 + 8 * h] = 1.f / l[h];
       }
       float* dst = sm_o + (size_t)(warp * 16 + n8 + 8 * h) * LDO + 2 * c4 * (DH / 8);
 #pragma unroll
@@ -360,28 +362,29 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_rows_kernel(const AttnQ8A
       const int r = i / (DH / 4), col = (i - r * (DH / 4)) * 4;
       float mr = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) mr = sm_l[w][r] == 0.f ? mr : fmaxf(mr, sm_m[w][r]);
+      for (int w = 0; w < kWarps; ++w) mr = fmaxf(mr, sm_lse[w][r]);
       float den = 0.f;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        if (sm_l[w][r] == 0.f) continue;  // this warp had no keys
-        const float f = ex2(sm_m[w][r] - mr);
+        if (sm_lse[w][r] == -INFINITY) continue;  // this warp had no keys
+        const float f0 = ex2(sm_lse[w][r] - mr), f = f0 * sm_inv[w][r];
         const float4 x = *reinterpret_cast<const float4*>(sm_o + (size_t)(w * 16 + r) * LDO + col);
-        den = fmaf(f, sm_l[w][r], den);
+        den += f0;
         acc.x = fmaf(f, x.x, acc.x);
         acc.y = fmaf(f, x.y, acc.y);
         acc.z = fmaf(f, x.z, acc.z);
         acc.w = fmaf(f, x.w, acc.w);
       }
+      const float inv = 1.f / den;
+      acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
       if (whole) {
-        const float inv = 1.f / den;
         uint16_t* dst = a.out + (((size_t)ub * a.S + r / a.G) * a.Hq + ug * a.G + r % a.G) * DH + col;
-        *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv),
-                                                    pack_bf16x2(acc.z * inv, acc.w * inv));
+        *reinterpret_cast<uint2*>(dst) =
+            make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
       } else {
         reinterpret_cast<float4*>(a.part_o)[(slot * 16 + r) * (DH / 4) + col / 4] = acc;
-        if (col == 0) reinterpret_cast<float2*>(a.part_ml)[slot * 16 + r] = make_float2(mr, den);
+        if (col == 0) a.part_lse[slot * 16 + r] = mr + log2f(den);
       }
     }
     __syncthreads();  // before the next segment's results
@@ -402,22 +405,22 @@ __global__ void __launch_bounds__(512) attn_q8_rows_merge_kernel(const AttnQ8Arg
   float mr = -INFINITY, den = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int c0 = uc.x; c0 <= uc.y; c0 += 4) {
-    float2 ml[4];
+    float lse[4];
     float4 x[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const size_t rec = ((size_t)u + min(c0 + k, uc.y)) * 16 + r;
-      ml[k] = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + rec);
+      lse[k] = __ldcg(a.part_lse + rec);
       x[k] = __ldcg(reinterpret_cast<const float4*>(a.part_o) + (rec << dv_log) + v);
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       // past the last record, or one without keys (its output was never written)
-      if (c0 + k > uc.y || ml[k].y == 0.f) continue;
-      const float mn = ml[k].x > mr ? ml[k].x : mr;
-      const float f0 = ex2(mr - mn), f1 = ex2(ml[k].x - mn);
+      if (c0 + k > uc.y || lse[k] == -INFINITY) continue;
+      const float mn = lse[k] > mr ? lse[k] : mr;
+      const float f0 = ex2(mr - mn), f1 = ex2(lse[k] - mn);
       mr = mn;
-      den = fmaf(den, f0, ml[k].y * f1);
+      den = fmaf(den, f0, f1);
       acc.x = fmaf(acc.x, f0, x[k].x * f1);
       acc.y = fmaf(acc.y, f0, x[k].y * f1);
       acc.z = fmaf(acc.z, f0, x[k].z * f1);

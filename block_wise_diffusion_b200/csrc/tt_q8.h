@@ -94,9 +94,10 @@ struct AttnQ8Args {
   int s_per_half, rows_per_half, halves, n_qtiles, units, n_ctas;
   int g_shift;      // G = 2^g_shift
   int2* unit_span;  // [units] first and last CTA that hold tiles of the unit
-  float* part_o;   // [units + n_ctas - 1] unnormalised outputs of segments:
-                   // [dh/4][256 rows][4], or [16 rows][dh] (at most 16 rows)
-  float* part_ml;  // [units + n_ctas - 1][256 or 16 rows][2]: maximum (log2 units), sum
+  float* part_o;    // [units + n_ctas - 1] outputs of segments:
+                    // [dh/4][256 rows][4], or [16 rows][dh] (at most 16 rows)
+  float* part_lse;  // [units + n_ctas - 1][256 or 16 rows]: log2 of the segment's sum of
+                    // 2^score; -inf without keys (its output is then never written)
   int* err;
 };
 cudaError_t launch_attn_q8(const AttnQ8Args& a, int type, cudaStream_t st);

@@ -433,6 +433,9 @@ typedef struct {
  *                   that hold a position below ctx_len[b] are finite and > 0
  *                   (v_scale at least 2^-60, as tt_append_ctx_q8 writes them);
  *                   other scales and codes are never used
+ *                   (a v_scale below 2^-100 of the largest one of its sequence and
+ *                   head, and own values below 2^-114, may count as larger or as
+ *                   rounded: values move by at most 2^-85 of that scale and 2^-125)
  *   ws              workspace of at least tt_workspace_bytes(d, TT_WS_ATTN_Q8)
  * A ctx_len outside 0..L_cap is clamped and recorded (TT_ERR_INVALID_ARG).
  * Calls that may overlap on the GPU need workspaces of their own.

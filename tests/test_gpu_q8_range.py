@@ -1,0 +1,100 @@
+"""tt_block_denoise_attn_q8 over the range of magnitudes that its inputs may have:
+scores, keys, values and scales near the ends of fp32.
+
+Bounds are relative to what a row adds up (no fixed term): half a bf16 step of the
+output, the fp16 rounding of every probability, twice the error of a score, and a few
+fp32 roundings (tests/_q8.py has the same terms); beside them what fp16 drops of a
+probability and of an own value, relative to the largest value that a row may read:
+a probability below fp16's normal numbers is off by at most 2^-25 times the key's
+code, which is at most 2^7 (2^15 for an own key), where the row's largest probability
+is at least 2^12, and its code 2^7 where its block holds the largest value: 2^-37 of that
+value (2^-29).  An own value has steps of at least 2^-124 (fp16's smallest times
+2^-100, the smallest power of two that its tile may carry)."""
+import numpy as np
+import pytest
+import torch
+
+import block_wise_diffusion_b200 as tt
+import tt_inputs
+from oracle import q8_oracle as Q
+from tests import _q8 as H
+
+pytestmark = pytest.mark.gpu
+
+
+def bound(out, mass, reach, d, ctx_len, v_blk, vd):
+    top = np.empty((d.B, 1, d.Hq, 1))
+    for b in range(d.B):
+        for h in range(d.Hq):
+            g = h * d.Hkv // d.Hq
+            top[b, 0, h, 0] = max(np.abs(v_blk[b, :, g]).max(),
+                                  np.abs(vd[b, g, :ctx_len[b]]).max(initial=0.0))
+    n = np.asarray(ctx_len, np.float64).reshape(-1, 1, 1, 1)
+    return (np.abs(out) * H.U16
+            + mass * (H.U_P + 2 * (d.dh + 8) * 2.0 ** -22 * reach + 2.0 ** -16)
+            + top * (d.S * 2.0 ** -29 + n * 2.0 ** -37) + 2.0 ** -125)
+
+
+def check(S, G, dh, kind, block, q, k, v, kc, ks, vc, vs, ctx_len, splits=(0,)):
+    """q, k, v: float64 arrays of bf16 numbers; the caches with their scales."""
+    B, Hkv, cap = kc.shape[:3]
+    d = tt_inputs.Dims(B=B, S=S, Hq=Hkv * G, Hkv=Hkv, dh=dh, V=512, L_cap=cap, ctx=("fixed", cap))
+    q, k, v = (H.bf16(x) for x in (q, k, v))
+    kd, vd = Q.dequantise_cache(kc, ks, kind, block), Q.dequantise_cache(vc, vs, kind, block)
+    out, mass, reach = Q.attention(q[0], k[0], v[0], kd, vd, ctx_len)
+    limit = bound(out, mass, reach, d, ctx_len, v[0], vd)
+    for n in splits:
+        tt.tt_set_attn_splits(n)
+        try:
+            got, ws = H.run_attention(d, tt.q8(kind, block), kind, (q[1], k[1], v[1]), kc, ks, vc, vs,
+                                      ctx_len)
+            assert tt.tt_device_status(ws) == 0
+        finally:
+            tt.tt_set_attn_splits(0)
+        got = got.float().cpu().numpy().astype(np.float64)
+        assert np.isfinite(got).all(), n
+        err = np.abs(got - out)
+        assert (err <= limit).all(), (n, np.nanmax(err / limit))
+    return got
+
+
+def inputs(seed, B, S, G, Hkv, dh, fq=1.0, fk=1.0, fv=1.0):
+    rng = np.random.default_rng(seed)
+    return rng, [rng.standard_normal((B, S, h, dh)) * f
+                 for h, f in ((Hkv * G, fq), (Hkv, fk), (Hkv, fv))]
+
+
+# more than 16 query rows per KV head, and at most 16: two kernels
+SHAPES = [(16, 4, 64), (32, 16, 128), (1, 16, 128), (1, 1, 64)]
+KINDS = [("int8", 64), ("e4m3", 16)]
+
+
+# ------------------------------------------ values far apart, far down, far up
+@pytest.mark.parametrize("kind,block", KINDS)
+@pytest.mark.parametrize("S,G,dh", SHAPES)
+@pytest.mark.parametrize("fv", [2.0 ** -80, 2.0 ** -110, 2.0 ** -113, 2.0 ** -120, 0.0])
+def test_tiny_own_values(kind, block, S, G, dh, fv):
+    """Without a context, with one, and with CTAs that hold one tile each, so that
+    the own keys are a record of their own."""
+    rng, (q, k, v) = inputs(4, 2, S, G, 1, dh, fv=fv)
+    for cap, cl in ((0, [0, 0]), (256, [256, 256]), (256, [1, 130])):
+        kc, ks = H.cache(rng, 2, 1, cap, dh, kind, block)
+        vc, vs = H.cache(rng, 2, 1, cap, dh, kind, block)
+        check(S, G, dh, kind, block, q, k, v, kc, ks, vc, vs, cl, (0, 1, 6, 40))
+
+
+@pytest.mark.parametrize("kind,block", KINDS)
+@pytest.mark.parametrize("S,G,dh", SHAPES)
+@pytest.mark.parametrize("big", [2.0 ** 20, 2.0 ** 60, 2.0 ** 110])
+@pytest.mark.parametrize("own", [2.0 ** -104, 1.0, 2.0 ** 100])
+@pytest.mark.parametrize("big_first", [True, False])
+def test_value_scales_far_apart(kind, block, S, G, dh, big, own, big_first):
+    """Blocks of zero values under the smallest scale beside very large values, own
+    values of either kind: what a key weighs does not depend on its value."""
+    rng, (q, k, v) = inputs(5, 2, S, G, 1, dh, fv=own)
+    kc, ks = H.cache(rng, 2, 1, 320, dh, kind, block)
+    vc, vs = H.cache(rng, 2, 1, 320, dh, kind, block, big)
+    zero = np.arange(320) >= 192 if big_first else np.arange(320) < 192
+    vc[:, :, zero] = 0
+    vs[:, :, zero[::block]] = Q.FLOOR
+    check(S, G, dh, kind, block, q, k, v, kc, ks, vc, vs, [320, 250], (0, 1, 8, 40))
