@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
           lds4f(sc + 64, *reinterpret_cast<float(*)[4]>(&iw[0]));
           lds4f(sc + 80, *reinterpret_cast<float(*)[4]>(&iw[4]));
 #pragma unroll
-          for (int g = 0; g < 8; ++g) kf[g] *= c_row;
+          for (int g = 0; g < 8; ++g) kf[g] = score_factor(c_row, kf[g]);
           if (!mbar_wait_inline(&s_full[ch], (uint32_t)pt & 1u, a.err, abort_flag,
                                 WHERE_ATTN_SOFTMAX)) {
             ok = false;

@@ -128,7 +128,15 @@ __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) 
 // (clamped so that 2^e and 2^-e are normal; 0 for zero and for non-finite).
 __device__ __forceinline__ int norm_exp(uint32_t amax) {
   const int e = (int)(amax >> 7);
-  return e == 0 || e == 255 ? 0 : min(max(e - 127 - 14, -126), 126);
+  return amax == 0 || e == 255 ? 0 : min(max(e - 127 - 14, -126), 126);
+}
+
+// Factor of a row's scores with a group of keys: the row's c times the keys' scale
+// k, held above 0, because a masked score is -inf and -inf * 0 is NaN.  2^-126
+// stands for anything below: the products that it multiplies are below 2^38.
+// (Positive floats and the NaN of a product are ordered as integers are.)
+__device__ __forceinline__ float score_factor(float c, float k) {
+  return __int_as_float(max(__float_as_int(c * k), 0x00800000));
 }
 
 // Ranges.  With m the running maximum of s_j + log2 w_j, a key's part of the row

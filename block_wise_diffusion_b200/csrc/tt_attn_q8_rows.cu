@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_rows_kernel(const AttnQ8A
         for (int h = 0; h < 2; ++h) {
           const float y = fmaxf(fmaxf(s[2 * g][2 * h], s[2 * g][2 * h + 1]),
                                 fmaxf(s[2 * g + 1][2 * h], s[2 * g + 1][2 * h + 1]));
-          mx[h] = fmaxf(mx[h], fmaf(y, c_row[h] * sk[g], lw[g]));
+          mx[h] = fmaxf(mx[h], fmaf(y, score_factor(c_row[h], sk[g]), lw[g]));
         }
       bool need = false;
       float alpha[2];
@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_rows_kernel(const AttnQ8A
         uint32_t p[4];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const float cg = c_row[h] * sk[g], off = lw[g] - m[h];
+          const float cg = score_factor(c_row[h], sk[g]), off = lw[g] - m[h];
           const float p0 = ex2(fmaf(s[2 * g][2 * h], cg, off));
           const float p1 = ex2(fmaf(s[2 * g][2 * h + 1], cg, off));
           const float p2 = ex2(fmaf(s[2 * g + 1][2 * h], cg, off));

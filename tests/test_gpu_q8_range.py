@@ -69,6 +69,49 @@ SHAPES = [(16, 4, 64), (32, 16, 128), (1, 16, 128), (1, 1, 64)]
 KINDS = [("int8", 64), ("e4m3", 16)]
 
 
+# ------------------------------------------------- scores that all but vanish
+@pytest.mark.parametrize("kind,block", KINDS)
+@pytest.mark.parametrize("S,G,dh", SHAPES)
+@pytest.mark.parametrize("fq", [2.0 ** -64, 2.0 ** -75, 2.0 ** -100, 2.0 ** -124])
+def test_tiny_queries_and_a_zero_key_block(kind, block, S, G, dh, fq):
+    """The keys' last block is zeros under the smallest scale, in a tile that the
+    context's end cuts."""
+    rng, (q, k, v) = inputs(1, 2, S, G, 2, dh, fq)
+    kc, ks = H.cache(rng, 2, 2, 300, dh, kind, block)
+    vc, vs = H.cache(rng, 2, 2, 300, dh, kind, block)
+    for b, n in enumerate((200, 131)):
+        at = (n - 1) // block
+        kc[b, :, at * block:] = 0
+        ks[b, :, at:] = Q.FLOOR
+    check(S, G, dh, kind, block, q, k, v, kc, ks, vc, vs, [200, 131], (0, 3))
+
+
+@pytest.mark.parametrize("kind,block", KINDS)
+@pytest.mark.parametrize("S,G,dh", SHAPES)
+@pytest.mark.parametrize("scale", [2.0 ** -120, 2.0 ** -135, 2.0 ** -149])
+def test_tiny_key_scales(kind, block, S, G, dh, scale):
+    rng, (q, k, v) = inputs(2, 2, S, G, 1, dh)
+    kc, ks = H.cache(rng, 2, 1, 200, dh, kind, block)
+    vc, vs = H.cache(rng, 2, 1, 200, dh, kind, block)
+    ks[:, :, 1:] = np.float32(scale)
+    check(S, G, dh, kind, block, q, k, v, kc, ks, vc, vs, [200, 77])
+
+
+@pytest.mark.parametrize("kind,block", KINDS)
+@pytest.mark.parametrize("S,G,dh", SHAPES)
+@pytest.mark.parametrize("fq,fk", [(2.0 ** -62, 2.0 ** -62), (2.0 ** -80, 2.0 ** -80),
+                                   (2.0 ** -120, 2.0 ** -120), (1.0, 2.0 ** -126),
+                                   (2.0 ** -129, 2.0 ** 124), (2.0 ** 124, 2.0 ** -129)])
+def test_tiny_own_keys(kind, block, S, G, dh, fq, fk):
+    """Without a context, and with one whose keys are zeros.  (The last two
+    pairs multiply to ordinary scores.)"""
+    rng, (q, k, v) = inputs(3, 2, S, G, 1, dh, fq, fk)
+    for cap, cl in ((0, [0, 0]), (140, [140, 0])):
+        kc, ks = H.cache(rng, 2, 1, cap, dh, kind, block, 0.0)
+        vc, vs = H.cache(rng, 2, 1, cap, dh, kind, block)
+        check(S, G, dh, kind, block, q, k, v, kc, ks, vc, vs, cl, (0, 2))
+
+
 # ------------------------------------------ values far apart, far down, far up
 @pytest.mark.parametrize("kind,block", KINDS)
 @pytest.mark.parametrize("S,G,dh", SHAPES)
