@@ -3,11 +3,12 @@
 // Per query row, with s_j = q . k_j / sqrt(dh) (log2 units), v scale w_j and
 // codes c_j:  out = sum_j 2^(s_j) w_j c_j / sum_j 2^(s_j).
 // One pass: p_j = 2^(s_j + log2 w_j - m) with m a running maximum of s_j +
-// log2 w_j, O = sum p_j c_j, l = sum p_j / w_j, out = O / l.  The key scale
-// multiplies a score and the value scale adds log2 w_j to its exponent, both
-// per group of 16 keys, so neither costs an instruction per element; p_j <=
-// 2^8 whatever the scales, which lets P be fp16 (11 bits: its rounding is an
-// eighth of the output's).
+// log2 w_j less kPeak, O = sum p_j c_j, l = sum p_j / w_j, out = O / l.  The key
+// scale multiplies a score and the value scale adds log2 w_j to its exponent, both
+// per group of 16 keys, so neither costs an instruction per element; p_j <= 2^15
+// and the row's largest at least 2^10, whatever the scales, which lets P be fp16:
+// its rounding is an eighth of the output's for keys down to 2^-24 of the largest
+// product, absolute below (2^-35 of it) (tt_attn_q8.cuh has the constants).
 //
 // Both products run on the tensor cores in fp16 (kind::f16): every int8 and
 // e4m3 code is an fp16 number; a query row and the block's own bf16 keys and
@@ -54,7 +55,6 @@ constexpr int kThreads = 512;
 constexpr int kConv = 128;                  // converter threads
 constexpr int kSlots = 2;                   // depth of the K and of the V ring
 constexpr uint32_t kSub = kAttnBN * 128;    // 128 rows x 64 fp16: 16 KB
-constexpr float kRescale = 8.0f;            // log2 units the running maximum may lag
 
 struct Smem {
   uint32_t q, k, v, raw, scales, bars, total;
@@ -404,12 +404,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
               mx = fmaxf(mx, fmaf(fmaxf(y0, y1), kf[g], lw[g]));
             }
           }
-          need = mx > m + kRescale;
+          need = mx > m + kTop;
           if (need) {
-            const float half = ex2(0.5f * (m - mx));
+            const float half = ex2(0.5f * (m - (mx - kPeak)));
             alpha = half * half;
             l = l * half * half;
-            m = mx;
+            m = mx - kPeak;
           }
           exps16(s, kf[0], lw[0], iw[0], c_row, m, l, p0);
           exps16(s + 16, kf[1], lw[1], iw[1], c_row, m, l, p1);

@@ -31,7 +31,6 @@ namespace {
 
 constexpr int kWarps = 8, kThreads = kWarps * 32;
 constexpr int NG = 2, kGroup = 16 * NG;  // keys per step of a warp
-constexpr float kRescale = 8.0f;    // log2 units the running maximum may lag
 
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                          uint32_t b1) {
@@ -122,11 +121,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_rows_kernel(const AttnQ8A
         mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
         mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
         alpha[h] = 1.f;
-        if (mx[h] > m[h] + kRescale) {
-          const float half = ex2(0.5f * (m[h] - mx[h]));
+        if (mx[h] > m[h] + kTop) {
+          const float half = ex2(0.5f * (m[h] - (mx[h] - kPeak)));
           alpha[h] = half * half;
           l[h] = l[h] * half * half;
-          m[h] = mx[h];
+          m[h] = mx[h] - kPeak;
           need = true;
         }
       }

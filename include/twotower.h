@@ -422,8 +422,9 @@ typedef struct {
  *   key_j = k_scale[b,g,j/block] * k_ctx[b,g,j,:] and the matching values for
  * the context positions j < ctx_len[b]; the block's own keys and values stay
  * bf16.  Scores, softmax statistics and the output are accumulated in fp32;
- * the probabilities are rounded to fp16 for the product with V.  The result
- * is the bf16 rounding of that.
+ * the probabilities, times their keys' value scales, are rounded to fp16 for the
+ * product with V (11 bits; below 2^-24 of a row's largest, to steps of 2^-34 of it).
+ * The result is the bf16 rounding of that.
  *
  *   f               format of the cache
  *   q_blk, k_blk, v_blk, ctx_len, out   as in tt_block_denoise_attn

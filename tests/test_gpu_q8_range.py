@@ -7,8 +7,8 @@ fp32 roundings (tests/_q8.py has the same terms); beside them what fp16 drops of
 probability and of an own value, relative to the largest value that a row may read:
 a probability below fp16's normal numbers is off by at most 2^-25 times the key's
 code, which is at most 2^7 (2^15 for an own key), where the row's largest probability
-is at least 2^12, and its code 2^7 where its block holds the largest value: 2^-37 of that
-value (2^-29).  An own value has steps of at least 2^-124 (fp16's smallest times
+is at least 2^10, and its code 2^7 where its block holds the largest value: 2^-35 of that
+value (2^-27).  An own value has steps of at least 2^-124 (fp16's smallest times
 2^-100, the smallest power of two that its tile may carry)."""
 import numpy as np
 import pytest
@@ -21,6 +21,8 @@ from tests import _q8 as H
 
 pytestmark = pytest.mark.gpu
 
+LOG2E = 1.4426950408889634
+
 
 def bound(out, mass, reach, d, ctx_len, v_blk, vd):
     top = np.empty((d.B, 1, d.Hq, 1))
@@ -32,7 +34,7 @@ def bound(out, mass, reach, d, ctx_len, v_blk, vd):
     n = np.asarray(ctx_len, np.float64).reshape(-1, 1, 1, 1)
     return (np.abs(out) * H.U16
             + mass * (H.U_P + 2 * (d.dh + 8) * 2.0 ** -22 * reach + 2.0 ** -16)
-            + top * (d.S * 2.0 ** -29 + n * 2.0 ** -37) + 2.0 ** -125)
+            + top * (d.S * 2.0 ** -27 + n * 2.0 ** -35) + 2.0 ** -125)
 
 
 def check(S, G, dh, kind, block, q, k, v, kc, ks, vc, vs, ctx_len, splits=(0,)):
@@ -141,3 +143,26 @@ def test_value_scales_far_apart(kind, block, S, G, dh, big, own, big_first):
     vc[:, :, zero] = 0
     vs[:, :, zero[::block]] = Q.FLOOR
     check(S, G, dh, kind, block, q, k, v, kc, ks, vc, vs, [320, 250], (0, 1, 8, 40))
+
+
+# --------------------------------------------------------- a peaked row
+@pytest.mark.parametrize("kind,block", KINDS)
+@pytest.mark.parametrize("S,G,dh", [(16, 4, 64), (1, 16, 128)])
+@pytest.mark.parametrize("down", [17.0, 26.0, 31.0])
+@pytest.mark.parametrize("at", [0, 40000])
+def test_one_peak_over_a_long_context(kind, block, S, G, dh, down, at):
+    """One key of value 0 takes nearly all the weight; 65536 others, each 2^-down of
+    it, make the output."""
+    L, cap = 65536, 65600
+    kc = np.zeros((1, 1, cap, dh), np.int8 if kind == "int8" else np.uint8)
+    vc = np.empty_like(kc)
+    ks = np.full((1, 1, -(-cap // block)), 1 / 64, np.float32)
+    vs = np.ones_like(ks)
+    one = np.float32(1.0)
+    vc[:] = Q.encode(np.ones(1), one, kind)[0]
+    kc[0, 0, at] = Q.encode(np.ones(1), one, kind)[0]
+    vc[0, 0, at] = 0
+    # q . k / sqrt(dh) = sqrt(dh) * scale: `down` in log2 units
+    ks[0, 0, at // block] = down / LOG2E / np.sqrt(dh)
+    q, k, v = (np.full((1, S, h, dh), x) for h, x in ((G, 1.0), (1, 0.0), (1, 1.0)))
+    check(S, G, dh, kind, block, q, k, v, kc, ks, vc, vs, [L], (0, 7))
