@@ -25,7 +25,7 @@ struct TileWalk {
   int off;          // tile within the unit
   int len;          // sequence b's context length, loaded when b is reached
   // The next segment: unit (b, k), local tiles [a, e), context length L.
-  __device__ __forceinline__ bool next(int& sb, int& sk, int& a, int& e, int& L) {
+  __host__ __device__ __forceinline__ bool next(int& sb, int& sk, int& a, int& e, int& L) {
     if (left <= 0) return false;
     L = min(max(len, 0), L_cap);
     const int n = 1 + (L + kAttnBN - 1) / kAttnBN;
@@ -50,7 +50,7 @@ struct PlanSmem {
 };
 
 // First tile of CTA c, floor(c T / P) (P <= 1024: no product leaves 32 bits).
-__device__ __forceinline__ int cta_first(int c, int T, int P) {
+__host__ __device__ __forceinline__ int cta_first(int c, int T, int P) {
   const int base = T / P;
   return c * base + c * (T - base * P) / P;
 }
@@ -116,9 +116,20 @@ __device__ __forceinline__ TileWalk plan_walk(const AttnQ8Args& a, PlanSmem& sm)
 
 // Recorded for the merge by the CTAs that hold a unit's first and last tile: all
 // CTAs between have a record (an empty range inside the unit an empty one).
-__device__ __forceinline__ void put_span(const AttnQ8Args& a, size_t u, bool first, bool last) {
-  if (first) a.unit_span[u].x = blockIdx.x;
-  if (last) a.unit_span[u].y = blockIdx.x;
+__host__ __device__ __forceinline__ void put_span(int2* unit_span, size_t u, int cta, bool first,
+                                                  bool last) {
+  if (first) unit_span[u].x = cta;
+  if (last) unit_span[u].y = cta;
+}
+// The spans of all segments of a CTA's walk.
+__host__ __device__ __forceinline__ void put_spans(int2* unit_span, TileWalk walk, int cta) {
+  int b, k, lo, hi, L;
+  while (walk.next(b, k, lo, hi, L))
+    put_span(unit_span, (size_t)b * walk.U + k, cta, lo == 0, hi == 1 + (L + kAttnBN - 1) / kAttnBN);
+}
+// What a merge may read of a launch of n_ctas CTAs.
+__host__ __device__ __forceinline__ bool span_in_range(int2 s, int n_ctas) {
+  return s.x >= 0 && s.x <= s.y && s.y < n_ctas;
 }
 
 // 2^e, e in [-126, 127]

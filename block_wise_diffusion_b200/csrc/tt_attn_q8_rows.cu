@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_rows_kernel(const AttnQ8A
     __syncthreads();
     const size_t slot = pair + blockIdx.x;
     const bool ends = sb == 1 + (L + kAttnBN - 1) / kAttnBN, whole = sa == 0 && ends;
-    if (threadIdx.x == 0) put_span(a, pair, sa == 0, ends);
+    if (threadIdx.x == 0) put_span(a.unit_span, pair, blockIdx.x, sa == 0, ends);
     for (int i = threadIdx.x; i < rows * (DH / 4); i += kThreads) {
       const int r = i / (DH / 4), col = (i - r * (DH / 4)) * 4;
       float mr = -INFINITY;
