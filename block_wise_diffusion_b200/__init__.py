@@ -451,6 +451,15 @@ def _arg(x, name: str, nbytes: int, dev: int) -> int | None:
     return x.data_ptr()
 
 
+def _codes_arg(x, name: str, nbytes: int, dev: int, f: Q8) -> int | None:
+    """_arg for 8-bit codes: a tensor has the format's type, or is plain bytes (uint8)."""
+    if x is not None and type(x) is not int and x.dtype != _torch.uint8:
+        want = {TT_Q8_INT8: _torch.int8, TT_Q8_E4M3: _torch.float8_e4m3fn}.get(f.type, x.dtype)
+        if x.dtype != want:
+            raise ValueError(f"{name} is {x.dtype}, the format's codes are {want}")
+    return _arg(x, name, nbytes, dev)
+
+
 def _raw_stream(stream, dev: int) -> int | None:
     if stream is None:
         return _torch._C._cuda_getCurrentRawStream(dev) if dev >= 0 else _stream(None)
@@ -460,7 +469,7 @@ def _raw_stream(stream, dev: int) -> int | None:
 def tt_block_denoise_attn_q8(d: Dims, f: Q8, q_blk, k_blk, v_blk, k_ctx, v_ctx, k_scale, v_scale,
                              ctx_len, out, ws, stream=None) -> None:
     """tt_block_denoise_attn over a context cache held in 8 bits: codes
-    [B, Hkv, L_cap, dh] (int8 or float8_e4m3fn) and one float32 scale per
+    [B, Hkv, L_cap, dh] (int8 or float8_e4m3fn as f has it, or their bytes) and one float32 scale per
     `f.block` positions and KV head."""
     B, S, Hq, Hkv, dh, L_cap, block = d.B, d.S, d.Hq, d.Hkv, d.dh, d.L_cap, f.block
     q, kv, ctx = 2 * B * S * Hq * dh, 2 * B * S * Hkv * dh, B * Hkv * L_cap * dh
@@ -468,8 +477,8 @@ def tt_block_denoise_attn_q8(d: Dims, f: Q8, q_blk, k_blk, v_blk, k_ctx, v_ctx, 
     dev = _device()
     code = lib().tt_block_denoise_attn_q8(
         d, f, _arg(q_blk, "q_blk", q, dev), _arg(k_blk, "k_blk", kv, dev),
-        _arg(v_blk, "v_blk", kv, dev), _arg(k_ctx, "k_ctx", ctx, dev),
-        _arg(v_ctx, "v_ctx", ctx, dev), _arg(k_scale, "k_scale", ns, dev),
+        _arg(v_blk, "v_blk", kv, dev), _codes_arg(k_ctx, "k_ctx", ctx, dev, f),
+        _codes_arg(v_ctx, "v_ctx", ctx, dev, f), _arg(k_scale, "k_scale", ns, dev),
         _arg(v_scale, "v_scale", ns, dev), _arg(ctx_len, "ctx_len", 4 * B, dev),
         _arg(out, "out", q, dev), _arg(ws, "ws", 0, dev), _nbytes(ws), _raw_stream(stream, dev))
     if code:
@@ -505,7 +514,7 @@ def tt_append_ctx_q8(d: Dims, f: Q8, n: int, new_len, k_new, v_new, k_ctx, v_ctx
         raise ValueError(f"k_new and v_new need the same strides; got {st} and {sv}")
     code = lib().tt_append_ctx_q8(
         d, f, n, _arg(new_len, "new_len", 4 * B, dev), k_ptr, v_ptr, _RowStrides(*st),
-        _arg(k_ctx, "k_ctx", ctx, dev), _arg(v_ctx, "v_ctx", ctx, dev),
+        _codes_arg(k_ctx, "k_ctx", ctx, dev, f), _codes_arg(v_ctx, "v_ctx", ctx, dev, f),
         _arg(k_scale, "k_scale", ns, dev), _arg(v_scale, "v_scale", ns, dev),
         _arg(ctx_len, "ctx_len", 4 * B, dev), _arg(ws, "ws", 0, dev), _nbytes(ws),
         _raw_stream(stream, dev))
