@@ -177,11 +177,11 @@ __device__ __forceinline__ void lds4f(uint32_t addr, float (&v)[4]) {
 }
 
 // 16 of a row's scores to probabilities, as fp16 pairs, and their part of the
-// row sum.  kf: key scale, lw: log2 of the value scale, iw: its inverse.
-__device__ __forceinline__ void exps16(const uint32_t* s, float kf, float lw, float iw, float c_row,
-                                       float m, float& l, uint32_t (&p)[8]) {
-  const float c = kf, off = lw - m;
-  const uint64_t c2 = pack2(c, c), o2 = pack2(off, off);
+// row sum.  kf: the row's score factor, lw: log2 of the value scale, iw: its inverse.
+__device__ __forceinline__ void exps16(const uint32_t* s, float kf, float lw, float iw, float m,
+                                       float& l, uint32_t (&p)[8]) {
+  const float off = lw - m;
+  const uint64_t c2 = pack2(kf, kf), o2 = pack2(off, off);
   uint64_t sum = 0;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
@@ -411,8 +411,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
             l = l * half * half;
             m = mx - kPeak;
           }
-          exps16(s, kf[0], lw[0], iw[0], c_row, m, l, p0);
-          exps16(s + 16, kf[1], lw[1], iw[1], c_row, m, l, p1);
+          exps16(s, kf[0], lw[0], iw[0], m, l, p0);
+          exps16(s + 16, kf[1], lw[1], iw[1], m, l, p1);
           // P and O are the tensor core's until P . V of the turn before has run
           if (i > first && !mbar_wait_inline(&pv_done[ch], (uint32_t)(pt - 1) & 1u, a.err,
                                              abort_flag, WHERE_ATTN_SOFTMAX)) {
@@ -436,17 +436,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_q8_kernel(const AttnQ8Args a
           }
           tmem_st8(tP, p0);
           tmem_st8(tP + 8, p1);
-          exps16(s + 32, kf[2], lw[2], iw[2], c_row, m, l, p0);
+          exps16(s + 32, kf[2], lw[2], iw[2], m, l, p0);
           tmem_st8(tP + 16, p0);
-          exps16(s + 48, kf[3], lw[3], iw[3], c_row, m, l, p1);
+          exps16(s + 48, kf[3], lw[3], iw[3], m, l, p1);
           tmem_st8(tP + 24, p1);
-          exps16(s + 64, kf[4], lw[4], iw[4], c_row, m, l, p0);
+          exps16(s + 64, kf[4], lw[4], iw[4], m, l, p0);
           tmem_st8(tP + 32, p0);
-          exps16(s + 80, kf[5], lw[5], iw[5], c_row, m, l, p1);
+          exps16(s + 80, kf[5], lw[5], iw[5], m, l, p1);
           tmem_st8(tP + 40, p1);
-          exps16(s + 96, kf[6], lw[6], iw[6], c_row, m, l, p0);
+          exps16(s + 96, kf[6], lw[6], iw[6], m, l, p0);
           tmem_st8(tP + 48, p0);
-          exps16(s + 112, kf[7], lw[7], iw[7], c_row, m, l, p1);
+          exps16(s + 112, kf[7], lw[7], iw[7], m, l, p1);
           tmem_st8(tP + 56, p1);
           tmem_wait_st();
           tc_fence_before();
