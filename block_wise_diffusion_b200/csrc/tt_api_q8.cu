@@ -149,9 +149,12 @@ LinearWs carve_linear(int rows, int K, void* ws) {
 // 128 columns are no more than the SMs, each tile goes to a cluster of `splits`
 // CTAs that share its K: of the shapes that fit, the one whose CTAs read the
 // fewest bytes, an exchange of partial sums counted as 200 KB (about 1 us).
-// 128 x 4608, K = 4096: 72 tiles of 64 in pairs 10.4 us, 144 of 32 alone 12.0,
-// 36 of 128 in fours 16.0 (clusters of four leave SMs of a GPC over, so not
-// all 36 run at once: more than two CTAs only within 7/8 of the SMs).
+// 128 x 4608, K = 4096: 72 tiles of 64 in pairs 10.6 us, 144 of 32 alone 12.2,
+// 36 of 128 in fours 16.3 (clusters of four leave SMs of a GPC over, so not
+// all 36 run at once: more than two CTAs only within 7/8 of the SMs).  64 x 1024, K =
+// 8192: 11.3, the best shape 10.6; 384 x 2304, K = 4096: 12.2, the best.  Clusters of
+// eight need more room than that bound leaves: 128 x 2048, K = 2048 takes 14.0 us with
+// 16 of them, 7.1 as 64 pairs on 32 columns; 256 x 1024, K = 4096 16.1 and 9.5.
 // splits = 0: more tiles than SMs; 256-wide tiles, one CTA each in turn, which
 // read A less often.
 struct I8Shape {
@@ -178,11 +181,13 @@ I8Shape i8_shape(int rows, int N, int K) {
 }
 
 // The persistent linear update: pairs of CTAs on 256-row tiles where there is more
-// than one 128-row tile (K = 4096; 2048 x 4608: 34.2 us against 37.5 for CTAs on
-// their own; 1024 x 6400: 32 against 39; 200 x 40000: 48 against 52), also where
-// the last pair has one (300 x 40000: 63 against 67; 384 x 20000: 41 against 39).  The vocabulary step, whose row count only the GPU knows,
-// keeps CTAs on their own: pairs gain 3 % at 1024 rows of 1024 and lose 20 % when
-// 100 of them are masked.
+// than one 128-row tile (K = 4096; 2048 x 4608: 34.3 us against 37.4 for CTAs on
+// their own; 1024 x 6400: 31 against 35; 200 x 40000: 46 against 51; 16384 x 4608: 252
+// against 293), also where the last pair has one 128-row tile and half of its work is
+// idle, which costs up to 10 % (300 x 40000: 63 against 61; 384 x 20000: 40 against
+// 36; 640 x 20000: 51 against 49).  The vocabulary step, whose row count only the GPU
+// knows, keeps CTAs on their own: pairs gain 3 % at 1024 rows of 1024 and lose 20 %
+// when 100 of them are masked.
 bool i8_pair(int rows) { return rows > kI8BM; }
 
 constexpr int kMaxRows = 1 << 24, kMaxK = 131072;

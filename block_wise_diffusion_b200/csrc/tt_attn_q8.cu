@@ -28,13 +28,13 @@
 // 4,900 cycles for the two chains where this order takes 3,500 to 3,900.
 // The block's own keys are a unit's last tile: their conversion from bf16 (two
 // passes, 13,000 cycles when nothing hides them) then runs under the softmax of
-// the tiles before (48 sequences of up to 32768 keys: 219 us; as first tile 239).
+// the tiles before (48 sequences of up to 32768 keys: 221 us; as first tile 20 more).
 // What bounds it: a tile of both chains is 2,050 cycles of tensor work and as many
 // of exponentials, but the hand-overs between the roles (S twice per tile through
 // one buffer, P to its product, the codes' reload and conversion) are loops of about
 // 3,200 cycles each: without exponentials, conversion and all but one MMA of eight,
 // the time falls by a quarter only.  4 sequences of 65536 int8 keys, S = 16, 2 KV heads of 16
-// queries and dh 128, with the merge: 78 us, 880 TFLOP/s and 1.7 TB/s of cache.
+// queries and dh 128, with the merge: 80 us, 860 TFLOP/s and 1.7 TB/s of cache.
 // Few tiles per CTA pay the start instead: 8 x 4096 keys, 32 us.
 // Roles (16 warps; registers are moved to the softmax by setmaxnreg):
 //   warps 0-3 / 4-7   softmax of chain 0 / 1;

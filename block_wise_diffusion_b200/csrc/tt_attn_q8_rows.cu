@@ -18,9 +18,12 @@
 // of its own (the formulas of tt_attn_q8.cu) and refills a register buffer as
 // soon as the products have read it.  The 8 warps' results are joined through
 // shared memory at a segment's end.
-// What bounds it: the instructions per key, most of them the codes' conversion.
-// 64 sequences of up to 8192 keys, 2 KV heads of 16 queries, dh 128, with the
-// merge: e4m3 46 us (3.0 TB/s), int8, whose conversion is longer, 49.
+// What bounds it: latency.  248 registers leave two warps to a scheduler, and a
+// warp's next keys are requested when the products have read its registers: 0.30
+// instructions per cycle and scheduler, no pipe above 28 %, DRAM at 35 %, the stalls
+// are loads and fixed latencies.  64 sequences of up to 8192 keys, 2 KV heads of 16
+// queries, dh 128, with the merge: e4m3 48 us (2.9 TB/s), int8, whose conversion is
+// longer, 52.
 #include <math.h>
 
 #include "tt_attn_q8.cuh"
